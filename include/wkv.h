@@ -375,6 +375,85 @@ WKV_API wkv_status wkv_v6_forward(int64_t B, int64_t T, int64_t H, int64_t D,
                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The gated linear recurrence: an unnormalised per-channel state with a gate
+ * for every token,
+ *     h_t = f_t h_{t-1} + i_t x_t,     out_t = h_t,
+ * where z gives the gate:
+ *     WKV_GATE_SIGMOID  f = sigmoid(z), i = 1 - f. z = -inf makes f = 0: the
+ *                       token starts a sequence of its own (packed rows);
+ *                       z = +inf keeps the state.
+ *     WKV_GATE_DECAY    f = e^{-z}, i = 1 (z as wkv_ext's w_t; z = +inf
+ *                       starts a sequence).
+ * NaN, and any other infinity, is out of contract. Like the WKV operators it
+ * takes whole sequences with the state in and out, single tokens, and has a
+ * backward.
+ *
+ *   x, z        [B, T, C] with the channel axis contiguous; the strides of the
+ *               batch and token axes are given in elements (>= 0; 0 repeats a
+ *               row), so x and z may be parts of one projection's output
+ *   dtypes      x F32: z and out F32. x BF16: z BF16 or F32, out BF16 or F32.
+ *   state       [B, C] fp32
+ *   checkpoints NULL, or [B, ceil(T / WKV_GATED_TILE), C] fp32: the forward
+ *               writes the state in front of every WKV_GATED_TILE tokens there
+ *   workspace   wkv_gated_workspace_size(B, T, C) bytes, 256-byte aligned,
+ *               zero-filled before its first use; not read and may be NULL when
+ *               T <= WKV_GATED_TILE. It serves forwards and backwards of any
+ *               shape that fits, one call at a time, and is kept apart from
+ *               the workspaces of the other operators. Its status word reports
+ *               device-side wait timeouts (wkv_query_status).
+ * The arithmetic and the state are fp32; 1 - f is carried where f is near 1.
+ * Results are bitwise reproducible. One launch.
+ */
+typedef enum { WKV_GATE_SIGMOID = 0, WKV_GATE_DECAY = 1 } wkv_gate;
+
+#define WKV_GATED_TILE 128
+
+/* Bytes of workspace wkv_gated_forward and wkv_gated_backward need (0 for
+ * invalid sizes: B, T, C >= 0, T < 2^24). Host-only. */
+WKV_API size_t wkv_gated_workspace_size(int64_t B, int64_t T, int64_t C);
+
+/*
+ * The recurrence over a sequence. out [B, T, C] contiguous, or NULL to compute
+ * the states alone; state_in NULL is the zero state; state_out NULL or [B, C],
+ * may be state_in. T = 0 passes the state through.
+ */
+WKV_API wkv_status wkv_gated_forward(int64_t B, int64_t T, int64_t C,
+                             const void *x, wkv_dtype x_dtype, int64_t x_batch_stride, int64_t x_token_stride,
+                             const void *z, wkv_dtype z_dtype, int64_t z_batch_stride, int64_t z_token_stride,
+                             wkv_gate gate, void *out, wkv_dtype out_dtype,
+                             const float *state_in, float *state_out, float *checkpoints,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradients, given gout = dL/d out [B, T, C] (contiguous, type g_dtype as
+ * out's) and dstate_out = dL/d state_out (NULL: zero):
+ *     D_t = gout_t + f_{t+1} D_{t+1}, with dstate_out added at the last token,
+ *     dx_t = i_t D_t,   dstate_in = f_1 D_1,
+ *     sigmoid: dz_t = D_t (h_{t-1} - x_t) f_t i_t;   decay: dz_t = -D_t h_{t-1} f_t.
+ * dx, dz contiguous [B, T, C] in the types of x and z; dstate_in NULL or
+ * [B, C] (may be dstate_out). checkpoints: as a forward of the same x, z and
+ * state_in wrote them; required when T > WKV_GATED_TILE, else not read.
+ */
+WKV_API wkv_status wkv_gated_backward(int64_t B, int64_t T, int64_t C,
+                              const void *x, wkv_dtype x_dtype, int64_t x_batch_stride, int64_t x_token_stride,
+                              const void *z, wkv_dtype z_dtype, int64_t z_batch_stride, int64_t z_token_stride,
+                              wkv_gate gate, const void *gout, wkv_dtype g_dtype,
+                              const float *state_in, const float *dstate_out, const float *checkpoints,
+                              void *dx, void *dz, float *dstate_in,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token for S streams: x, z [S, C] (channel axis contiguous, element
+ * stride of the stream axis given), out [S, C], state_in and state_out
+ * required, [S, C] fp32 (may be the same array). No workspace, no waits.
+ */
+WKV_API wkv_status wkv_gated_step(int64_t S, int64_t C,
+                          const void *x, wkv_dtype x_dtype, int64_t x_stride,
+                          const void *z, wkv_dtype z_dtype, int64_t z_stride,
+                          wkv_gate gate, void *out, wkv_dtype out_dtype,
+                          const float *state_in, float *state_out, void *stream);
+
+/*
  * wkv_forward without a caller-provided workspace. The pages have no
  * counterpart to this entry point; it exists for callers that cannot allocate
  * device memory themselves: hosts that hand a plug-in only its input and

@@ -1,0 +1,343 @@
+"""The gated linear recurrence on the GPU against its float64 oracle: forward,
+backward and step over types, gates, lengths around every tile edge, odd
+widths, strides, sequence starts, and the ways a program calls them."""
+import numpy as np
+import pytest
+import torch
+
+import wkv_recurrence_b200 as W
+from oracle import gated_oracle as G
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+TYPES = [(F32, F32, F32), (BF16, BF16, BF16), (BF16, BF16, F32), (BF16, F32, BF16), (BF16, F32, F32)]
+# half a step of the output's type, relative to the value
+HALF = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+
+
+def draw(B, T, C, xt, zt, gate, seed=0, starts=False, slow=False):
+    g = torch.Generator(device="cuda").manual_seed(1000 * T + C + seed)
+    x = torch.randn(B, T, C, generator=g, device="cuda").to(xt)
+    if gate == "sigmoid":
+        z = torch.randn(B, T, C, generator=g, device="cuda") * 2 + (8 if slow else 1)
+    else:
+        z = torch.exp(torch.rand(B, T, C, generator=g, device="cuda") * (2 if slow else 10.6) - 9.2)
+    z = z.to(zt)
+    if starts and T > 0:
+        at = torch.rand(B, T, generator=g, device="cuda") < 0.05
+        z[at] = -np.inf if gate == "sigmoid" else np.inf
+    h0 = torch.randn(B, C, generator=g, device="cuda")
+    return x, z, h0
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def check(got, ref, allowed, what):
+    half = HALF[got.dtype]
+    got = np64(got)
+    assert got.shape == ref.shape, what
+    lim = (np.abs(ref) + allowed) * half + allowed + 1e-37  # underflow: results below the smallest normal are flushed
+    bad = ~(np.abs(got - ref) <= lim)
+    assert not bad.any(), (what, int(bad.sum()), got[bad][:3], ref[bad][:3], lim[bad][:3])
+
+
+def check_forward(x, z, h0, gate, out, state):
+    ref, rst = G.forward(np64(x), np64(z), None if h0 is None else np64(h0), gate)
+    al, _ = G.allowed_forward(np64(x), np64(z), None if h0 is None else np64(h0), gate)
+    check(out, ref, al, "out")
+    if x.shape[1]:
+        check(state, rst, al[:, -1], "state")
+
+
+def check_backward(x, z, h0, g, ds, gate, got):
+    args = (np64(x), np64(z), None if h0 is None else np64(h0), np64(g), None if ds is None else np64(ds), gate)
+    for a, r, al, what in zip(got, G.backward(*args), G.allowed_backward(*args), ("dx", "dz", "dstate")):
+        check(a, r, al, what)
+
+
+@pytest.mark.parametrize("gate", ["sigmoid", "decay"])
+@pytest.mark.parametrize("xt,zt,ot", TYPES)
+@pytest.mark.parametrize("B,T,C", [(2, 1, 64), (1, 17, 3), (2, 128, 66), (3, 129, 65), (2, 517, 130)])
+def test_forward_and_backward(B, T, C, xt, zt, ot, gate):
+    x, z, h0 = draw(B, T, C, xt, zt, gate)
+    marks = W.gated_checkpoints(x)
+    out, state = W.gated_forward(x, z, h0, gate=gate, out_dtype=ot, checkpoints=marks)
+    assert out.dtype == ot
+    check_forward(x, z, h0, gate, out, state)
+    g = torch.randn(B, T, C, device="cuda").to(ot)
+    ds = torch.randn(B, C, device="cuda")
+    got = W.gated_backward(x, z, g, h0, ds, gate=gate, checkpoints=marks)
+    assert got[0].dtype == xt and got[1].dtype == zt
+    check_backward(x, z, h0, g, ds, gate, got)
+    again = W.gated_backward(x, z, g, h0, ds, gate=gate)  # without the forward's checkpoints
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 31, 32, 33, 112, 127, 128, 129, 143, 144, 145, 255, 256, 257, 2047, 2048,
+                               2049, 4113])
+@pytest.mark.parametrize("C", [1, 2, 33, 64])
+def test_lengths_and_widths(T, C):
+    x, z, h0 = draw(2, T, C, F32, F32, "sigmoid", seed=1)
+    out, state = W.gated_forward(x, z, h0)
+    check_forward(x, z, h0, "sigmoid", out, state)
+    g, ds = torch.randn_like(x), torch.randn_like(h0)
+    check_backward(x, z, h0, g, ds, "sigmoid", W.gated_backward(x, z, g, h0, ds))
+
+
+@pytest.mark.parametrize("gate", ["sigmoid", "decay"])
+@pytest.mark.parametrize("T", [5, 200, 3000])
+def test_sequence_starts_and_no_state(T, gate):
+    x, z, _ = draw(2, T, 40, F32, F32, gate, seed=2, starts=True)
+    z[0, 0] = -np.inf if gate == "sigmoid" else np.inf
+    z[1, T - 1] = -np.inf if gate == "sigmoid" else np.inf
+    out, state = W.gated_forward(x, z, gate=gate)
+    check_forward(x, z, None, gate, out, state)
+    g = torch.randn_like(x)
+    dx, dz, dh = W.gated_backward(x, z, g, gate=gate)
+    check_backward(x, z, None, g, None, gate, (dx, dz, dh))
+    assert torch.equal(dz[z.isinf()], torch.zeros_like(dz[z.isinf()]))  # nothing flows through a start
+    assert torch.equal(out[1, T - 1], x[1, T - 1])
+
+
+def test_a_held_state_passes_a_gate_of_infinity_exactly():
+    x, z, h0 = draw(1, 300, 64, F32, F32, "sigmoid")
+    z.fill_(np.inf)
+    out, state = W.gated_forward(x, z, h0)
+    assert torch.equal(out, h0[:, None].expand_as(out)) and torch.equal(state, h0)
+    zd = torch.zeros_like(x)
+    zd[:, ::2] = -0.0
+    out, state = W.gated_forward(torch.zeros_like(x), zd, h0, gate="decay")
+    assert torch.equal(out, h0[:, None].expand_as(out)) and torch.equal(state, h0)
+
+
+def test_constant_slow_gate_keeps_its_mean():
+    """1 - f = 1.2e-4 for 40000 tokens of a constant input: f in fp32 alone would be off by up to 2e-4."""
+    T = 40000
+    x = torch.ones(1, T, 34, device="cuda")
+    z = torch.full((1, T, 34), 9.0, device="cuda") + torch.arange(34, device="cuda") * 0.01
+    out, state = W.gated_forward(x, z)
+    check_forward(x, z, None, "sigmoid", out, state)
+    assert float((out[0, -1] - 1).abs().max()) < 1e-2
+    zd = torch.full((1, T, 34), 1e-4, device="cuda")
+    out, state = W.gated_forward(x, zd, gate="decay")
+    ref, _ = G.forward(np64(x), np64(zd), None, "decay")
+    # the sum's fixed point is 1 / (1 - f) = 1e4; the recurrence forgets errors over as many tokens
+    assert np.abs(np64(out) / ref - 1).max() < 1e4 * 2 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("T", [60, 300])
+def test_growing_decay(T):
+    x, z, h0 = draw(1, T, 8, F32, F32, "decay")
+    z = -0.05 * torch.rand_like(z)  # f > 1
+    out, state = W.gated_forward(x, z, h0, gate="decay")
+    check_forward(x, z, h0, "decay", out, state)
+
+
+@pytest.mark.parametrize("B,T,C", [(20, 300, 2048), (600, 140, 30), (1, 40000, 40)])
+def test_many_groups_and_long_rows(B, T, C):
+    x, z, h0 = draw(B, T, C, F32, F32, "sigmoid", slow=True)
+    marks = W.gated_checkpoints(x)
+    out, state = W.gated_forward(x, z, h0, checkpoints=marks)
+    g, ds = torch.randn_like(x), torch.randn_like(h0)
+    got = W.gated_backward(x, z, g, h0, ds, checkpoints=marks)
+    rows = slice(0, 2) if B > 2 else slice(0, 1)
+    cols = slice(0, min(C, 70))
+    cut = lambda t: t[rows][..., cols].contiguous()  # noqa: E731
+    check_forward(cut(x), cut(z), cut(h0), "sigmoid", cut(out), cut(state))
+    check_backward(cut(x), cut(z), cut(h0), cut(g), cut(ds), "sigmoid", [cut(t) for t in got])
+    last = slice(B - 1, B)
+    tail = slice(max(0, C - 33), C)
+    cut = lambda t: t[last][..., tail].contiguous()  # noqa: E731
+    check_forward(cut(x), cut(z), cut(h0), "sigmoid", cut(out), cut(state))
+    check_backward(cut(x), cut(z), cut(h0), cut(g), cut(ds), "sigmoid", [cut(t) for t in got])
+    out2, state2 = W.gated_forward(x, z, h0)
+    assert torch.equal(out, out2) and torch.equal(state, state2)  # bitwise reproducible
+    for a, b in zip(got, W.gated_backward(x, z, g, h0, ds, checkpoints=marks)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T", [100, 400])
+def test_strides_and_alignment(T):
+    B, C = 3, 66
+    both = torch.randn(B, T, 2 * C + 1, device="cuda").to(BF16)
+    for x, z in ((both[..., :C], both[..., C:2 * C]),              # halves of one projection, odd row pitch
+                 (both[..., 1:C + 1], both[..., C + 1:2 * C + 1]),  # a base that only fits one element
+                 (both.transpose(0, 1).contiguous().transpose(0, 1)[..., :C], both[..., C:2 * C]),  # time first
+                 (both[..., :C], both[:1, :, C:2 * C].expand(B, T, C)),  # one gate for all rows
+                 (both[..., :C], both[:, :1, C:2 * C].expand(B, T, C))):  # one gate for all tokens
+        out, state = W.gated_forward(x, z)
+        want, wst = W.gated_forward(x.contiguous(), z.contiguous())
+        check_forward(x, z, None, "sigmoid", out, state)
+        g = torch.randn(B, T, C, device="cuda").to(BF16)
+        check_backward(x, z, None, g, None, "sigmoid", W.gated_backward(x, z, g))
+        assert torch.equal(out, want) and torch.equal(state, wst)
+
+
+def test_time_of_zero_and_empty_batches():
+    h0 = torch.randn(2, 5, device="cuda")
+    e = torch.empty(2, 0, 5, device="cuda")
+    out, state = W.gated_forward(e, e, h0)
+    assert out.shape == (2, 0, 5) and torch.equal(state, h0)
+    assert torch.equal(W.gated_forward(e, e)[1], torch.zeros_like(h0))
+    dx, dz, dh = W.gated_backward(e, e, e, h0, h0)
+    assert dx.numel() == 0 and torch.equal(dh, h0)
+    for shape in ((0, 7, 5), (2, 7, 0)):
+        e = torch.empty(shape, device="cuda")
+        assert W.gated_forward(e, e)[0].shape == shape
+        assert W.gated_backward(e, e, e)[0].shape == shape
+    s = torch.empty(0, 4, device="cuda")
+    assert W.gated_step(s, s, s)[0].shape == (0, 4)
+
+
+@pytest.mark.parametrize("T", [20, 100, 300, 5000])
+def test_state_in_place_and_split(T):
+    x, z, h0 = draw(2, T, 96, F32, F32, "sigmoid")
+    out, state = W.gated_forward(x, z, h0)
+    s = h0.clone()
+    o2, s2 = W.gated_forward(x, z, s, state_out=s)
+    assert s2 is s and torch.equal(o2, out) and torch.equal(s, state)
+    k = T // 3  # hand the state over in the middle
+    a, s = W.gated_forward(x[:, :k], z[:, :k], h0)
+    b, s = W.gated_forward(x[:, k:], z[:, k:], s)
+    check_forward(x, z, h0, "sigmoid", torch.cat([a, b], 1), s)
+
+
+@pytest.mark.parametrize("gate", ["sigmoid", "decay"])
+@pytest.mark.parametrize("xt,zt,ot", TYPES)
+@pytest.mark.parametrize("S,C", [(1, 1), (5, 66), (64, 768), (3, 4100)])
+def test_step(S, C, xt, zt, ot, gate):
+    x, z, h0 = draw(S, 1, C, xt, zt, gate)
+    out, state = W.gated_step(h0, x[:, 0], z[:, 0], gate=gate, out_dtype=ot)
+    check_forward(x, z, h0, gate, out[:, None], state)
+    wide = torch.zeros(S, 2 * C + 1, device="cuda", dtype=xt)
+    wide[:, :C] = x[:, 0]
+    s = h0.clone()
+    o2, s2 = W.gated_step(s, wide[:, :C], z[:, 0], gate=gate, out_dtype=ot, inplace=True)
+    assert s2 is s and torch.equal(s, state) and torch.equal(o2, out)
+
+
+def test_steps_follow_the_sequence():
+    x, z, h0 = draw(3, 40, 64, F32, F32, "decay")
+    out, state = W.gated_forward(x, z, h0, gate="decay")
+    s = h0.clone()
+    for t in range(40):
+        o, s = W.gated_step(s, x[:, t], z[:, t], gate="decay", inplace=True)
+        al, _ = G.allowed_forward(np64(x), np64(z), np64(h0), "decay")
+        assert (np.abs(np64(o) - np64(out[:, t])) <= 2 * al[:, t] + 1e-6 * np.abs(np64(o))).all()
+
+
+def test_autograd_and_differences():
+    for gate in ("sigmoid", "decay"):
+        x, z, h0 = draw(2, 150, 4, F32, F32, gate, seed=9)
+        x, z, h0 = (t.requires_grad_() for t in (x, z, h0))
+        out, state = W.Gated.apply(x, z, h0, gate)
+        g, ds = torch.randn_like(out), torch.randn_like(state)
+        dx, dz, dh = torch.autograd.grad((out * g).sum() + (state * ds).sum(), (x, z, h0))
+        check_backward(x, z, h0, g, ds, gate, (dx, dz, dh))
+        # and against differences of the float64 forward: the central difference of step d is off by d^2/6 times a
+        # third derivative of order |gradient|, and by 2^-52 |loss| / d
+        args = [np64(t) for t in (x, z, h0)]
+        loss = lambda a: float((G.forward(*a, gate)[0] * np64(g)).sum() + (G.forward(*a, gate)[1] * np64(ds)).sum())  # noqa: E731
+        rng = np.random.default_rng(1)
+        for k, grad in enumerate((dx, dz, dh)):
+            for _ in range(4):
+                at = tuple(rng.integers(0, n) for n in args[k].shape)
+                d = 1e-4 * (1.0 if k != 1 or gate == "sigmoid" else max(1e-1, args[1][at]))
+                up, down = [a.copy() for a in args], [a.copy() for a in args]
+                up[k][at] += d
+                down[k][at] -= d
+                want = (loss(up) - loss(down)) / (2 * d)
+                assert abs(float(grad[at]) - want) <= 1e-4 * max(1.0, abs(want)), (gate, k, at)
+    # a shared gate's gradient is summed over what shares it; outputs that are not used give zeros
+    x, z, _ = draw(3, 140, 8, BF16, BF16, "sigmoid")
+    zs = z[:1].clone().requires_grad_()
+    out, _ = W.Gated.apply(x, zs.expand(3, 140, 8), None, "sigmoid")
+    out.float().sum().backward()
+    want = G.backward(np64(x), np64(z[:1].expand(3, 140, 8)), None, np.ones(x.shape), None, "sigmoid")[1].sum(0, keepdims=True)
+    al = G.allowed_backward(np64(x), np64(z[:1].expand(3, 140, 8)), None, np.ones(x.shape), None, "sigmoid")[1].sum(0, keepdims=True)
+    # three bf16 gradients, rounded once each and summed with two more bf16 roundings
+    mag = np.abs(G.backward(np64(x), np64(z[:1].expand(3, 140, 8)), None, np.ones(x.shape), None, "sigmoid")[1]).sum(0, keepdims=True)
+    assert (np.abs(np64(zs.grad) - want) <= 4 * 2.0 ** -8 * mag + al).all()
+    xr = x.clone().requires_grad_()
+    _, st = W.Gated.apply(xr, z, None, "sigmoid")
+    st.sum().backward()
+    check_backward(x, z, None, torch.zeros_like(x), torch.ones(3, 8, device="cuda"), "sigmoid",
+                   (xr.grad, *W.gated_backward(x, z, torch.zeros_like(x), None, torch.ones(3, 8, device="cuda"))[1:]))
+
+
+def test_one_workspace_over_shapes_and_directions():
+    ws = torch.zeros(W.gated_workspace_size(4, 3000, 200), dtype=torch.uint8, device="cuda")
+    for (B, T, C) in ((4, 3000, 200), (1, 700, 64), (2, 2500, 199), (4, 3000, 200)):
+        x, z, h0 = draw(B, T, C, F32, F32, "sigmoid")
+        marks = W.gated_checkpoints(x)
+        out, state = W.gated_forward(x, z, h0, workspace=ws, checkpoints=marks)
+        g = torch.randn_like(x)
+        got = W.gated_backward(x, z, g, h0, workspace=ws, checkpoints=marks)
+        assert W.query_status(ws) == 0
+        check_forward(x[:1], z[:1], h0[:1], "sigmoid", out[:1], state[:1])
+        check_backward(x[:1], z[:1], h0[:1], g[:1], None, "sigmoid", [t[:1] for t in got])
+
+
+def test_two_streams_at_once():
+    jobs = []
+    for i in range(2):
+        x, z, h0 = draw(2, 6000, 128, F32, F32, "sigmoid", seed=i)
+        jobs.append((x, z, h0, W.gated_forward(x, z, h0)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(5):
+        for i, (x, z, h0, _) in enumerate(jobs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(W.gated_forward(x, z, h0))
+    torch.cuda.synchronize()
+    for i, (_, _, _, want) in enumerate(jobs):
+        for out, state in got[i]:
+            assert torch.equal(out, want[0]) and torch.equal(state, want[1])
+
+
+def test_graphs_captured_on_one_stream_and_replayed_on_two():
+    jobs = []
+    side = torch.cuda.Stream()
+    for i in range(2):
+        x, z, h0 = draw(2, 5000, 128, F32, F32, "sigmoid", seed=i)
+        g = torch.randn_like(x)
+        marks = W.gated_checkpoints(x)
+        want = (*W.gated_forward(x, z, h0, checkpoints=marks), *W.gated_backward(x, z, g, h0, checkpoints=marks))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            m = W.gated_checkpoints(x)
+            got = (*W.gated_forward(x, z, h0, checkpoints=m), *W.gated_backward(x, z, g, h0, checkpoints=m))
+        jobs.append((graph, want, got, (x, z, h0, g)))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(4):
+        for s, (graph, *_) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, want, got, _ in jobs:
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    x = jobs[0][3][0]
+    x.copy_(torch.randn_like(x))  # new inputs in the captured tensors
+    jobs[0][0].replay()
+    torch.cuda.synchronize()
+    want = W.gated_forward(*jobs[0][3][:3])
+    assert torch.equal(jobs[0][2][0], want[0]) and torch.equal(jobs[0][2][1], want[1])
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose token stride puts the last elements past 2^31 elements of the base."""
+    T, C = 260, 64
+    pitch = (1 << 31) // 250
+    big = torch.empty(T * pitch, dtype=BF16, device="cuda")
+    x = big.as_strided((1, T, C), (0, pitch, 1))
+    z = torch.randn(1, T, C, device="cuda").to(BF16)
+    x.copy_(torch.randn(1, T, C, device="cuda"))
+    out, state = W.gated_forward(x, z)
+    check_forward(x, z, None, "sigmoid", out, state)

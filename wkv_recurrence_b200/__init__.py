@@ -9,6 +9,8 @@ binding:
     out, state = wkv_recurrence_b200.forward(k, v, w, u, state=None)
     out, state = wkv_recurrence_b200.forward_host(k_host, v_host, w, u)  # k, v in host memory
     out, state = wkv_recurrence_b200.step(state, k, v, w, u)
+    out, state = wkv_recurrence_b200.gated_forward(x, z, state)          # the gated linear recurrence
+    out, state = wkv_recurrence_b200.gated_step(state, x, z)
 
 Importing the package does not load the library; the first call does, and
 fails loudly if it is missing or no CUDA device is present.
@@ -17,7 +19,10 @@ fails loudly if it is missing or no CUDA device is present.
 from .api import (WKV, PreparedForward, PreparedStep, WkvError, backward, empty_state, forward,  # noqa: F401
                   forward_host, forward_host_buffer_size, forward_kernel, forward_launches, make_workspace,
                   query_status, step, v6_forward, workspace_size)
+from .gated import (Gated, gated_backward, gated_checkpoints, gated_forward, gated_step,  # noqa: F401
+                    gated_workspace_size)
 
 __all__ = ["forward", "forward_host", "forward_host_buffer_size", "step", "backward", "WKV", "v6_forward",
            "workspace_size", "forward_kernel", "forward_launches", "make_workspace", "query_status", "empty_state",
-           "PreparedForward", "PreparedStep", "WkvError"]
+           "PreparedForward", "PreparedStep", "WkvError", "gated_forward", "gated_backward", "gated_step",
+           "gated_checkpoints", "gated_workspace_size", "Gated"]

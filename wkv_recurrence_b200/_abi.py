@@ -25,11 +25,16 @@ WKV_ERR_BOUNDS = 7
 WKV_F32 = 0
 WKV_BF16 = 1
 
+WKV_GATE_SIGMOID = 0
+WKV_GATE_DECAY = 1
+WKV_GATED_TILE = 128  # tokens per checkpoint of the gated recurrence
+
 # entry points declared in include/wkv.h
 EXPORTS = ("wkv_forward_workspace_size", "wkv_forward_kernel", "wkv_forward_launches", "wkv_forward",
            "wkv_forward_ext", "wkv_step", "wkv_step_ext", "wkv_query_status", "wkv_status_string", "wkv_version",
            "wkv_forward_noalloc", "wkv_last_cuda_error", "wkv_backward_workspace_size", "wkv_backward",
-           "wkv_v6_forward", "wkv_forward_host_buffer_size", "wkv_forward_host")
+           "wkv_v6_forward", "wkv_forward_host_buffer_size", "wkv_forward_host", "wkv_gated_workspace_size",
+           "wkv_gated_forward", "wkv_gated_backward", "wkv_gated_step")
 
 # size of the library's built-in scratch array used by wkv_forward_noalloc
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -113,6 +118,16 @@ def lib() -> ctypes.CDLL:
         L.wkv_backward.restype = I
         L.wkv_v6_forward.argtypes = [I64, I64, I64, I64, P, P, P, P, I, P, I, P, P, P, SZ, P]
         L.wkv_v6_forward.restype = I
+        L.wkv_gated_workspace_size.argtypes = [I64, I64, I64]
+        L.wkv_gated_workspace_size.restype = SZ
+        # x and z: pointer, dtype, batch and token strides; then the gate
+        xz = [P, I, I64, I64, P, I, I64, I64, I]
+        L.wkv_gated_forward.argtypes = [I64, I64, I64, *xz, P, I, P, P, P, P, SZ, P]
+        L.wkv_gated_forward.restype = I
+        L.wkv_gated_backward.argtypes = [I64, I64, I64, *xz, P, I, P, P, P, P, P, P, P, SZ, P]
+        L.wkv_gated_backward.restype = I
+        L.wkv_gated_step.argtypes = [I64, I64, P, I, I64, P, I, I64, I, P, I, P, P, P]
+        L.wkv_gated_step.restype = I
         L.wkv_query_status.argtypes = [P, P]
         L.wkv_query_status.restype = I
         L.wkv_status_string.argtypes = [I]

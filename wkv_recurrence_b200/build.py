@@ -21,6 +21,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC_DIR = os.path.join(HERE, "csrc")
 MAIN = os.path.join(SRC_DIR, "wkv_api.cu")
+GATED = os.path.join(SRC_DIR, "wkv_gated.cu")
 HOST = os.path.join(SRC_DIR, "wkv_host.cpp")  # host-side streaming of host-resident sequences
 LIB = os.path.join(HERE, "_build", "libwkv.so")
 LIB_DEBUG = os.path.join(HERE, "_build", "libwkv_debug.so")
@@ -30,13 +31,14 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-    "-Xcompiler", "-Wall",
+    "-Xcompiler", "-Wall", "--threads", "4",
 ]
 
 
 def _sources():
     return sorted(glob.glob(os.path.join(SRC_DIR, "*.cu")) + glob.glob(os.path.join(SRC_DIR, "*.cuh"))
-                  + glob.glob(os.path.join(SRC_DIR, "*.cpp")) + [HEADER])
+                  + glob.glob(os.path.join(SRC_DIR, "*.cpp")) + glob.glob(os.path.join(SRC_DIR, "*.h"))
+                  + [HEADER])
 
 
 def nvcc() -> str:
@@ -53,7 +55,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return out
     os.makedirs(os.path.dirname(out), exist_ok=True)
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(["-DWKV_DEBUG"] if debug else []), *extra_flags, "-o", tmp, MAIN, HOST]
+    cmd = [nvcc(), *NVCC_FLAGS, *(["-DWKV_DEBUG"] if debug else []), *extra_flags, "-o", tmp, MAIN, GATED, HOST]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

@@ -18,14 +18,26 @@
 #include "wkv_cluster.cuh"
 #include "wkv_device.cuh"
 #include "wkv_fwd.cuh"
+#include "wkv_host_util.h"
 #include "wkv_step.cuh"
 #include "wkv_v6.cuh"
 
 namespace wkv {
 namespace {
+// The last CUDA error this library met in the calling thread (for
+// wkv_last_cuda_error), recorded wherever a call returns WKV_ERR_CUDA because
+// of one.
+thread_local cudaError_t g_last_cuda_error = cudaSuccess;
+}  // namespace
+
+bool cuda_ok(cudaError_t e) {
+  if (e != cudaSuccess) g_last_cuda_error = e;
+  return e == cudaSuccess;
+}
+
+namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;  // 1 s
 
 // ---------------------------------------------------------------------------
 // kernel configurations
@@ -72,22 +84,6 @@ struct Plan {
   size_t off_flags_a, off_flags_p, off_agg_a, off_agg_p, off_x0, off_wtot, bytes;
 };
 
-
-// The last CUDA error this library met in the calling thread (for
-// wkv_last_cuda_error), recorded wherever a call returns WKV_ERR_CUDA because
-// of one.
-thread_local cudaError_t g_last_cuda_error = cudaSuccess;
-
-bool cuda_ok(cudaError_t e) {
-  if (e != cudaSuccess) g_last_cuda_error = e;
-  return e == cudaSuccess;
-}
-
-// Status of the launch just made (<<<>>> launches report only through
-// cudaGetLastError).
-wkv_status launch_result() { return cuda_ok(cudaGetLastError()) ? WKV_OK : WKV_ERR_CUDA; }
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // The plan for a call: which kernel, tile sizes, and the workspace layout.
 // tma_ok = false (inputs that TMA cannot address: misaligned base, row pitch
@@ -388,7 +384,6 @@ bool make_tmap(CUtensorMap* m, const void* base, wkv_dtype dt, int64_t B, int64_
   return r == CUDA_SUCCESS;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // ---------------------------------------------------------------------------
 // launchers

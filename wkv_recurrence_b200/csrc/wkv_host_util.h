@@ -1,0 +1,25 @@
+// Host-side helpers shared by the library's translation units.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/wkv.h"
+
+namespace wkv {
+
+// Records a CUDA runtime error for wkv_last_cuda_error (defined in
+// wkv_api.cu); true for cudaSuccess.
+bool cuda_ok(cudaError_t e);
+
+// Status of the <<<>>> launch just made.
+inline wkv_status launch_result() { return cuda_ok(cudaGetLastError()) ? WKV_OK : WKV_ERR_CUDA; }
+
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+constexpr uint64_t kDefaultTimeoutNs = 1000000000ull;  // 1 s, the limit of every device-side wait
+
+}  // namespace wkv
