@@ -44,7 +44,8 @@ enum { kGateSigmoid = 0, kGateDecay = 1 };
 // token. So a gate is carried as one number c whose sign says which of f and
 // 1 - f it holds exactly to fp32:  c = -(1 - f) where 0 <= 1 - f < 1/2 (sign
 // bit set, also for 1 - f = 0), else c = f. With base = 1 or 0 accordingly,
-//     f h + b = c h + (base h + b),   f = base + c,   1 - f = (1 - base) - c.
+//     f h + b = base h + (c h + b),   f = base + c,   1 - f = (1 - base) - c,
+// and a slow gate rounds the large h once a token, not twice.
 
 // base: 1 where c holds f - 1, 0 where it holds f
 __device__ __forceinline__ float gate_base(float c) { return __float_as_int(c) < 0 ? 1.f : 0.f; }
@@ -72,10 +73,10 @@ __device__ __forceinline__ float gate_coef(float z) {
 
 // f h + b
 __device__ __forceinline__ float gate_step(float c, float base, float h, float b) {
-  return fmaf(c, h, fmaf(base, h, b));
+  return fmaf(base, h, fmaf(c, h, b));
 }
 // f p
-__device__ __forceinline__ float gate_mul(float c, float base, float p) { return fmaf(c, p, base * p); }
+__device__ __forceinline__ float gate_mul(float c, float base, float p) { return fmaf(base, p, c * p); }
 // what the token adds to the state, i_t x_t
 template <int GATE>
 __device__ __forceinline__ float gate_input(float c, float base, float x) {
