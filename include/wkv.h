@@ -454,6 +454,60 @@ WKV_API wkv_status wkv_gated_step(int64_t S, int64_t C,
                           const float *state_in, float *state_out, void *stream);
 
 /*
+ * RMS norm of the residual stream, by groups (heads) of a row. The v6 readout
+ * and the gated state have no denominator; the norm brings them back to a
+ * common size before the next projection. Per row of C columns, in `groups`
+ * equal parts:
+ *     s = x + residual, rounded to r_dtype (the type the stream is held in),
+ *     y = s (mean over the part of s^2 + eps)^-1/2 weight.
+ *
+ *   x, residual [N, C], rows at the given element strides, columns contiguous;
+ *               residual may be NULL (s = x, and `sum` is not written)
+ *   dtypes      x F32: residual and y F32. x BF16: residual and y BF16 or F32.
+ *   weight      [C] fp32
+ *   y, sum      contiguous [N, C]; sum takes s in r_dtype and may be residual
+ *               where that is contiguous
+ *   eps         positive;  groups  1..8192, dividing C
+ * Sums are fp32; results are bitwise reproducible. One launch. 16-byte aligned
+ * rows with C / groups a multiple of 8 take the fast kernels; any other
+ * alignment and size a slower one. N < 2^31, C < 2^24.
+ */
+WKV_API wkv_status wkv_rms_norm(int64_t N, int64_t C, int64_t groups, float eps,
+                        const void *x, wkv_dtype x_dtype, int64_t x_stride,
+                        const void *residual, wkv_dtype r_dtype, int64_t r_stride,
+                        const float *weight, void *y, wkv_dtype y_dtype, void *sum, void *stream);
+
+/*
+ * wkv_rms_norm with y in 8 bits: q [N, C] in e4m3 (contiguous) and scale
+ * [N, C / block] fp32, scale = max |y| / 448 over its block of columns (1 for
+ * a block of zeros), q = y / scale rounded to nearest even. block: 32, 64 or
+ * 128 and dividing C, or 0 (or C) for one scale per row.
+ */
+WKV_API wkv_status wkv_rms_norm_quant(int64_t N, int64_t C, int64_t groups, float eps,
+                              const void *x, wkv_dtype x_dtype, int64_t x_stride,
+                              const void *residual, wkv_dtype r_dtype, int64_t r_stride,
+                              const float *weight, void *q, float *scale, int64_t block, void *sum,
+                              void *stream);
+
+/*
+ * Gradients of wkv_rms_norm: with gy = dL/dy [N, C] (contiguous), s as `sum`
+ * holds it (or x, at row stride s_stride) and gsum = dL/ds of the stream's
+ * other reader (contiguous, s_dtype; NULL: zero), r = (mean s^2 + eps)^-1/2 and
+ * p = gy weight:
+ *     dsum = gsum + r (p - s r^2 mean(p s)),   dweight = sum over rows of gy s r.
+ * dsum [N, C] in s_dtype (the gradient of x and residual alike), dweight [C]
+ * fp32. gy F32: s F32; gy BF16: s BF16 or F32. workspace: at least
+ * wkv_rms_norm_backward_workspace_size bytes (0 for invalid sizes), 256-byte
+ * aligned, any contents. Two launches (three for sizes off the fast path).
+ */
+WKV_API size_t wkv_rms_norm_backward_workspace_size(int64_t N, int64_t C, int64_t groups);
+WKV_API wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps,
+                                 const void *gy, wkv_dtype gy_dtype,
+                                 const void *s, wkv_dtype s_dtype, int64_t s_stride,
+                                 const float *weight, const void *gsum, void *dsum, float *dweight,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * wkv_forward without a caller-provided workspace. The pages have no
  * counterpart to this entry point; it exists for callers that cannot allocate
  * device memory themselves: hosts that hand a plug-in only its input and

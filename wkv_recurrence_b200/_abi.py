@@ -34,7 +34,8 @@ EXPORTS = ("wkv_forward_workspace_size", "wkv_forward_kernel", "wkv_forward_laun
            "wkv_forward_ext", "wkv_step", "wkv_step_ext", "wkv_query_status", "wkv_status_string", "wkv_version",
            "wkv_forward_noalloc", "wkv_last_cuda_error", "wkv_backward_workspace_size", "wkv_backward",
            "wkv_v6_forward", "wkv_forward_host_buffer_size", "wkv_forward_host", "wkv_gated_workspace_size",
-           "wkv_gated_forward", "wkv_gated_backward", "wkv_gated_step")
+           "wkv_gated_forward", "wkv_gated_backward", "wkv_gated_step", "wkv_rms_norm", "wkv_rms_norm_quant",
+           "wkv_rms_norm_backward_workspace_size", "wkv_rms_norm_backward")
 
 # size of the library's built-in scratch array used by wkv_forward_noalloc
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -128,6 +129,16 @@ def lib() -> ctypes.CDLL:
         L.wkv_gated_backward.restype = I
         L.wkv_gated_step.argtypes = [I64, I64, P, I, I64, P, I, I64, I, P, I, P, P, P]
         L.wkv_gated_step.restype = I
+        # N, C, groups, eps; x and residual: pointer, dtype, row stride; weight
+        norm = [I64, I64, I64, ctypes.c_float, P, I, I64, P, I, I64, P]
+        L.wkv_rms_norm.argtypes = [*norm, P, I, P, P]
+        L.wkv_rms_norm.restype = I
+        L.wkv_rms_norm_quant.argtypes = [*norm, P, P, I64, P, P]
+        L.wkv_rms_norm_quant.restype = I
+        L.wkv_rms_norm_backward_workspace_size.argtypes = [I64, I64, I64]
+        L.wkv_rms_norm_backward_workspace_size.restype = SZ
+        L.wkv_rms_norm_backward.argtypes = [I64, I64, I64, ctypes.c_float, P, I, P, I, I64, P, P, P, P, P, SZ, P]
+        L.wkv_rms_norm_backward.restype = I
         L.wkv_query_status.argtypes = [P, P]
         L.wkv_query_status.restype = I
         L.wkv_status_string.argtypes = [I]

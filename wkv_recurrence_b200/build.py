@@ -22,6 +22,7 @@ ROOT = os.path.dirname(HERE)
 SRC_DIR = os.path.join(HERE, "csrc")
 MAIN = os.path.join(SRC_DIR, "wkv_api.cu")
 GATED = os.path.join(SRC_DIR, "wkv_gated.cu")
+NORM = os.path.join(SRC_DIR, "wkv_norm.cu")
 HOST = os.path.join(SRC_DIR, "wkv_host.cpp")  # host-side streaming of host-resident sequences
 LIB = os.path.join(HERE, "_build", "libwkv.so")
 LIB_DEBUG = os.path.join(HERE, "_build", "libwkv_debug.so")
@@ -55,7 +56,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
         return out
     os.makedirs(os.path.dirname(out), exist_ok=True)
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(["-DWKV_DEBUG"] if debug else []), *extra_flags, "-o", tmp, MAIN, GATED, HOST]
+    cmd = [nvcc(), *NVCC_FLAGS, *(["-DWKV_DEBUG"] if debug else []), *extra_flags, "-o", tmp, MAIN, GATED, NORM, HOST]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

@@ -1,0 +1,286 @@
+// C ABI of the RMS norm (declared in include/wkv.h): argument checks, the
+// choice of kernel, workspace layout and launches of wkv_norm.cuh. Nothing
+// here allocates device memory.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "wkv_host_util.h"
+#include "wkv_norm.cuh"
+
+namespace wkv {
+namespace {
+
+using bf = __nv_bfloat16;
+constexpr int kSms = 148;
+constexpr int64_t kMaxGroups = 8192;  // wkv_norm_row keeps one float per group in shared memory
+
+size_t elem(int d) { return d == WKV_F32 ? 4 : 2; }
+bool dtype_ok(int d) { return d == WKV_F32 || d == WKV_BF16; }
+
+bool sizes_ok(int64_t N, int64_t C, int64_t G) {
+  if (N < 0 || C < 0 || G < 1 || G > kMaxGroups || C % G != 0) return false;
+  return N < (1ll << 31) && C < (1ll << 24);
+}
+
+// Rows that start on 16 bytes.
+bool rows_ok(const void* p, int dt, int64_t stride) { return aligned(p, 16) && (stride * (int64_t)elem(dt)) % 16 == 0; }
+
+// The team that holds a group of n8 vectors: TW lanes (0: a whole CTA of
+// `threads`) with K vectors each. K = 0: too wide for registers.
+struct Team {
+  int TW, K, threads;
+};
+
+Team fwd_team(int64_t n8) {
+  if (n8 <= 32) {
+    // a power of two of lanes, or three vectors on a quarter as many where
+    // that leaves none idle (96 columns: 4 lanes x 3 against 12 of 16 lanes)
+    int tw = 4;
+    while (tw < n8) tw *= 2;
+    if (n8 * 4 == 3ll * tw && tw >= 16) return Team{tw / 4, 3, 256};
+    return Team{tw, 1, 256};
+  }
+  if (n8 <= 128) return Team{32, (int)((n8 + 31) / 32), 256};
+  const int K = n8 <= 1024 ? 1 : n8 <= 2048 ? 2 : 4;
+  if (n8 > 4096) return Team{0, 0, 0};
+  return Team{0, K, (int)round_up((size_t)((n8 + K - 1) / K), 32)};
+}
+
+Team bwd_team(int64_t n8, int64_t G) {
+  Team t{0, 0, 0};
+  if (n8 <= 64) {
+    int tw = 4;
+    while (tw < n8 && tw < 32) tw *= 2;
+    if (tw * G <= 512) return Team{tw, n8 > 32 ? 2 : 1, 0};
+  }
+  if (G == 1 && n8 <= 2048) {
+    t.K = n8 <= 1024 ? 1 : 2;
+    t.threads = (int)round_up((size_t)((n8 + t.K - 1) / t.K), 32);
+  }
+  return t;
+}
+
+struct BwdPlan {
+  Team team;
+  int rpc, threads, nparts;  // team kernel
+  int gparts;                // general kernels
+  size_t off_rstd, bytes;
+};
+
+bool bwd_plan(int64_t N, int64_t C, int64_t G, BwdPlan* pl) {
+  if (!sizes_ok(N, C, G)) return false;
+  const int64_t D = C / G;
+  pl->team = D % 8 == 0 ? bwd_team(D / 8, G) : Team{0, 0, 0};
+  pl->nparts = 0;
+  if (pl->team.K) {
+    if (pl->team.TW) {
+      const int tpr = pl->team.TW * (int)G;
+      pl->rpc = std::max(1, 256 / tpr);
+      pl->threads = (int)round_up((size_t)pl->rpc * tpr, 32);
+    } else {
+      pl->rpc = 1;
+      pl->threads = pl->team.threads;
+    }
+    const int per_sm = std::max(1, 1024 / pl->threads);
+    pl->nparts = (int)std::max<int64_t>(1, std::min<int64_t>((N + pl->rpc - 1) / pl->rpc, (int64_t)kSms * per_sm));
+  }
+  pl->gparts = (int)std::max<int64_t>(1, std::min<int64_t>(N, 256));
+  const size_t parts = (size_t)std::max(pl->nparts, pl->gparts) * (size_t)C;
+  pl->off_rstd = round_up(sizeof(float) * parts, 256);
+  pl->bytes = std::max<size_t>(256, pl->off_rstd + sizeof(float) * (size_t)(N * G));
+  return true;
+}
+
+template <typename X, typename R, bool RES, int TW, int K>
+void launch_team(const NormParams& p, int threads, cudaStream_t st) {
+  const long long segs = p.N * p.G;
+  const unsigned grid = (unsigned)(TW ? (segs * TW + 255) / 256 : segs);
+  wkv_norm_team<X, R, RES, TW, K><<<grid, threads, 0, st>>>(p);
+}
+
+template <typename X, typename R, bool RES>
+void fwd_shape(const NormParams& p, const Team& t, cudaStream_t st) {
+  switch (t.TW * 8 + t.K) {
+    case 4 * 8 + 1: return launch_team<X, R, RES, 4, 1>(p, t.threads, st);
+    case 4 * 8 + 3: return launch_team<X, R, RES, 4, 3>(p, t.threads, st);
+    case 8 * 8 + 1: return launch_team<X, R, RES, 8, 1>(p, t.threads, st);
+    case 8 * 8 + 3: return launch_team<X, R, RES, 8, 3>(p, t.threads, st);
+    case 16 * 8 + 1: return launch_team<X, R, RES, 16, 1>(p, t.threads, st);
+    case 32 * 8 + 1: return launch_team<X, R, RES, 32, 1>(p, t.threads, st);
+    case 32 * 8 + 2: return launch_team<X, R, RES, 32, 2>(p, t.threads, st);
+    case 32 * 8 + 3: return launch_team<X, R, RES, 32, 3>(p, t.threads, st);
+    case 32 * 8 + 4: return launch_team<X, R, RES, 32, 4>(p, t.threads, st);
+    case 1: return launch_team<X, R, RES, 0, 1>(p, t.threads, st);
+    case 2: return launch_team<X, R, RES, 0, 2>(p, t.threads, st);
+    default: return launch_team<X, R, RES, 0, 4>(p, t.threads, st);
+  }
+}
+
+// A general row kernel may use 48 KB of shared memory without asking.
+static_assert(kMaxGroups * sizeof(float) <= 40 * 1024, "one float per group");
+
+wkv_status norm(int64_t N, int64_t C, int64_t G, float eps, const void* x, int x_dtype, int64_t x_stride, const void* res,
+                int r_dtype, int64_t r_stride, const float* weight, void* y, int out_kind, void* s, float* scale,
+                int64_t block, void* stream) {
+  if (!sizes_ok(N, C, G)) return WKV_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return WKV_ERR_INVALID_ARG;
+  if (!dtype_ok(x_dtype) || (res && !dtype_ok(r_dtype)) || (res && x_dtype == WKV_F32 && r_dtype != WKV_F32))
+    return WKV_ERR_UNSUPPORTED_DTYPE;
+  if (x_stride < 0 || r_stride < 0 || x_stride > (1ll << 31) || r_stride > (1ll << 31)) return WKV_ERR_INVALID_ARG;
+  if (out_kind == kOutE4m3) {
+    if (block == 0) block = C;
+    if (block != C && ((block != 32 && block != 64 && block != 128) || C % block != 0)) return WKV_ERR_INVALID_ARG;
+  }
+  if (N == 0 || C == 0) return WKV_OK;
+  if (!x || !weight || !y || (res && !s) || (out_kind == kOutE4m3 && !scale)) return WKV_ERR_INVALID_ARG;
+  if (!aligned(x, elem(x_dtype)) || !aligned(weight, 4) || (out_kind == kOutF32 && !aligned(y, 4)) ||
+      (out_kind == kOutBf16 && !aligned(y, 2)) || (res && (!aligned(res, elem(r_dtype)) || !aligned(s, elem(r_dtype)))) ||
+      (out_kind == kOutE4m3 && !aligned(scale, 4)))
+    return WKV_ERR_MISALIGNED;
+  NormParams p;
+  std::memset(&p, 0, sizeof p);
+  p.N = N;
+  p.C = (int)C;
+  p.G = (int)G;
+  p.D = (int)(C / G);
+  p.eps = eps;
+  p.x = x;
+  p.x_st = x_stride;
+  p.res = res;
+  p.res_st = r_stride;
+  p.weight = weight;
+  p.y = y;
+  p.out_kind = out_kind;
+  p.s = res ? s : nullptr;
+  p.scale = scale;
+  p.block = (int)block;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Team t{0, 0, 0};
+  const int64_t D = p.D;
+  if (D % 8 == 0 && rows_ok(x, x_dtype, x_stride) && (!res || (rows_ok(res, r_dtype, r_stride) && aligned(s, 16))) &&
+      aligned(weight, 16) && aligned(y, 16) && N * G * 32 < (1ll << 38))
+    t = fwd_team(D / 8);
+  const int width = t.TW ? t.TW : t.threads;
+  if (out_kind == kOutE4m3 && block != D && (D % block != 0 || block / 8 > width)) t.K = 0;
+  if (t.K && N * G < (1ll << 31)) {
+    if (!res) {
+      if (x_dtype == WKV_F32) fwd_shape<float, float, false>(p, t, st);
+      else fwd_shape<bf, bf, false>(p, t, st);
+    } else if (x_dtype == WKV_F32) {
+      fwd_shape<float, float, true>(p, t, st);
+    } else if (r_dtype == WKV_F32) {
+      fwd_shape<bf, float, true>(p, t, st);
+    } else {
+      fwd_shape<bf, bf, true>(p, t, st);
+    }
+  } else {
+    wkv_norm_row<<<(unsigned)N, 256, sizeof(float) * (size_t)G, st>>>(p, x_dtype == WKV_BF16, r_dtype == WKV_BF16);
+  }
+  return launch_result();
+}
+
+template <typename Y, typename S, bool GS>
+void bwd_shape(const NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
+  const size_t smem = pl.rpc > 1 ? sizeof(float) * (size_t)p.C : 0;
+  const unsigned grid = (unsigned)pl.nparts;
+  switch (pl.team.TW * 8 + pl.team.K) {
+    case 4 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 4, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
+    case 8 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 8, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
+    case 16 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 16, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
+    case 32 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 32, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
+    case 32 * 8 + 2: wkv_norm_bwd_team<Y, S, GS, 32, 2><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
+    case 1: wkv_norm_bwd_team<Y, S, GS, 0, 1><<<grid, pl.threads, 0, st>>>(p, 1); break;
+    default: wkv_norm_bwd_team<Y, S, GS, 0, 2><<<grid, pl.threads, 0, st>>>(p, 1); break;
+  }
+}
+
+}  // namespace
+}  // namespace wkv
+
+using namespace wkv;
+
+extern "C" {
+
+wkv_status wkv_rms_norm(int64_t N, int64_t C, int64_t groups, float eps, const void* x, wkv_dtype x_dtype, int64_t x_stride,
+                        const void* residual, wkv_dtype r_dtype, int64_t r_stride, const float* weight, void* y,
+                        wkv_dtype y_dtype, void* sum, void* stream) {
+  if (!dtype_ok(y_dtype) || (x_dtype == WKV_F32 && y_dtype != WKV_F32)) return WKV_ERR_UNSUPPORTED_DTYPE;
+  return norm(N, C, groups, eps, x, x_dtype, x_stride, residual, r_dtype, r_stride, weight, y,
+              y_dtype == WKV_F32 ? kOutF32 : kOutBf16, sum, nullptr, 0, stream);
+}
+
+wkv_status wkv_rms_norm_quant(int64_t N, int64_t C, int64_t groups, float eps, const void* x, wkv_dtype x_dtype,
+                              int64_t x_stride, const void* residual, wkv_dtype r_dtype, int64_t r_stride,
+                              const float* weight, void* q, float* scale, int64_t block, void* sum, void* stream) {
+  return norm(N, C, groups, eps, x, x_dtype, x_stride, residual, r_dtype, r_stride, weight, q, kOutE4m3, sum, scale, block,
+              stream);
+}
+
+size_t wkv_rms_norm_backward_workspace_size(int64_t N, int64_t C, int64_t groups) {
+  BwdPlan pl;
+  return bwd_plan(N, C, groups, &pl) ? pl.bytes : 0;
+}
+
+wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps, const void* gy, wkv_dtype gy_dtype,
+                                 const void* sum, wkv_dtype s_dtype, int64_t s_stride, const float* weight, const void* gsum,
+                                 void* dsum, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  BwdPlan pl;
+  if (!bwd_plan(N, C, groups, &pl)) return WKV_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return WKV_ERR_INVALID_ARG;
+  if (!dtype_ok(gy_dtype) || !dtype_ok(s_dtype) || (gy_dtype == WKV_F32 && s_dtype != WKV_F32))
+    return WKV_ERR_UNSUPPORTED_DTYPE;
+  if (s_stride < 0 || s_stride > (1ll << 31)) return WKV_ERR_INVALID_ARG;
+  if (C == 0) return WKV_OK;
+  if (!weight || !dweight) return WKV_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (N == 0) return cuda_ok(cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)C, st)) ? WKV_OK : WKV_ERR_CUDA;
+  if (!gy || !sum || !dsum || !workspace) return WKV_ERR_INVALID_ARG;
+  if (workspace_bytes < pl.bytes) return WKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 256) || !aligned(gy, elem(gy_dtype)) || !aligned(sum, elem(s_dtype)) ||
+      !aligned(dsum, elem(s_dtype)) || (gsum && !aligned(gsum, elem(s_dtype))) || !aligned(weight, 4) || !aligned(dweight, 4))
+    return WKV_ERR_MISALIGNED;
+  NormBwdParams p;
+  std::memset(&p, 0, sizeof p);
+  p.N = N;
+  p.C = (int)C;
+  p.G = (int)groups;
+  p.D = (int)(C / groups);
+  p.eps = eps;
+  p.gy = gy;
+  p.s = sum;
+  p.s_st = s_stride;
+  p.weight = weight;
+  p.gs = gsum;
+  p.ds = dsum;
+  p.part = static_cast<float*>(workspace);
+  p.rstd = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + pl.off_rstd);
+  const bool team = pl.team.K && aligned(gy, 16) && rows_ok(sum, s_dtype, s_stride) && (!gsum || aligned(gsum, 16)) &&
+                    aligned(dsum, 16) && aligned(weight, 16);
+  p.nparts = team ? pl.nparts : pl.gparts;
+  if (team) {
+    if (gy_dtype == WKV_F32) {
+      if (gsum) bwd_shape<float, float, true>(p, pl, st);
+      else bwd_shape<float, float, false>(p, pl, st);
+    } else if (s_dtype == WKV_F32) {
+      if (gsum) bwd_shape<bf, float, true>(p, pl, st);
+      else bwd_shape<bf, float, false>(p, pl, st);
+    } else {
+      if (gsum) bwd_shape<bf, bf, true>(p, pl, st);
+      else bwd_shape<bf, bf, false>(p, pl, st);
+    }
+  } else {
+    wkv_norm_bwd_row<<<(unsigned)N, 256, 0, st>>>(p, gy_dtype == WKV_BF16, s_dtype == WKV_BF16);
+    wkv_norm_bwd_cols<<<dim3((unsigned)((C + 255) / 256), (unsigned)p.nparts), 256, 0, st>>>(p, gy_dtype == WKV_BF16,
+                                                                                             s_dtype == WKV_BF16);
+  }
+  if (launch_result() != WKV_OK) return WKV_ERR_CUDA;
+  wkv_norm_bwd_join<<<(unsigned)((C + 31) / 32), 256, 0, st>>>(p.part, p.nparts, p.C, dweight);
+  return launch_result();
+}
+
+}  // extern "C"
