@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "wkv_gated.cuh"
 #include "wkv_host_util.h"
@@ -17,24 +18,23 @@ namespace {
 constexpr int kGatedL = WKV_GATED_TILE;  // tokens per tile of a sequence of several tiles
 constexpr int kGatedJ = 16;              // tokens per warp
 constexpr int kGatedNW = kGatedL / kGatedJ;
+constexpr int kMaxDevices = 64;
 
 struct GatedPlan {
-  int V, NG, nch, G, ngrp, NW;
+  int NG, nch, G, ngrp, NW;
   long long tiles;
   size_t off_tot, off_pre, bytes;
 };
 
 // Sizes as wkv_forward's: B, T, C >= 0, T < 2^24, B*T*C < 2^62; and fewer than
 // 2^31 tiles.
-bool gated_plan(int64_t B, int64_t T, int64_t C, int V, GatedPlan* pl) {
+bool gated_plan(int64_t B, int64_t T, int64_t C, GatedPlan* pl) {
   if (B < 0 || T < 0 || C < 0) return false;
-  if (T >= (1ll << 24) || C >= (1ll << 31) || B >= (1ll << 31)) return false;
+  if (T >= (1ll << 24) || C >= (1ll << 31) - kGatedCG || B >= (1ll << 31)) return false;
   if (B > 0 && C > 0 && T > (int64_t)((1ull << 62) / (uint64_t)(B * C))) return false;
-  const int64_t CG = 32 * V;
-  const int64_t NG = (C + CG - 1) / CG, nch = (T + kGatedL - 1) / kGatedL;
+  const int64_t NG = (C + kGatedCG - 1) / kGatedCG, nch = (T + kGatedL - 1) / kGatedL;
   const int64_t items = B * NG;
   if (items >= (1ll << 31) || (items > 0 && nch > (int64_t)(((1ll << 31) - 1) / items))) return false;
-  pl->V = V;
   pl->NG = (int)NG;
   pl->nch = (int)nch;
   pl->NW = nch > 1 ? kGatedNW : (int)std::max<int64_t>(1, (T + kGatedJ - 1) / kGatedJ);
@@ -46,9 +46,9 @@ bool gated_plan(int64_t B, int64_t T, int64_t C, int V, GatedPlan* pl) {
   pl->tiles = items * nch;
   size_t off = sizeof(WsHeader);
   pl->off_tot = off;
-  if (nch > 1 && pl->G > 1) off = round_up(off + sizeof(GatedRec) * (size_t)(items * nch * CG), 256);
+  if (nch > 1 && pl->G > 1) off = round_up(off + sizeof(GatedRec) * (size_t)(items * nch * kGatedCG), 256);
   pl->off_pre = off;
-  if (nch > 1) off = round_up(off + sizeof(GatedRec) * (size_t)(items * pl->ngrp * CG), 256);
+  if (nch > 1) off = round_up(off + sizeof(GatedRec) * (size_t)(items * pl->ngrp * kGatedCG), 256);
   pl->bytes = off;
   return true;
 }
@@ -60,34 +60,76 @@ bool types_ok(int x, int z, int o) {
 
 size_t elem(int d) { return d == WKV_F32 ? 4 : 2; }
 
-// Whether V adjacent channels can move as one access: base and strides.
 bool vec_ok(const void* p, int dt, int V, int64_t s0 = 0, int64_t s1 = 0) {
   return aligned(p, elem(dt) * V) && s0 % V == 0 && s1 % V == 0;
 }
 
+// The widest copy (16, 4 or 2 bytes) that base, strides and row length allow.
+int granule(const void* p, int dt, int64_t C, int64_t s0, int64_t s1) {
+  const int64_t es = (int64_t)elem(dt);
+  for (const int g : {16, 4})
+    if (aligned(p, g) && C * es % g == 0 && s0 * es % g == 0 && s1 * es % g == 0) return g;
+  return 2;
+}
+
+// CTAs to launch: as many as are resident at once, at most one per tile. The
+// kernel's shared memory limit is raised and its occupancy looked up once per
+// device.
+struct Resident {
+  std::mutex mu;
+  int ctas[kMaxDevices] = {};
+};
+
+template <typename F>
+bool resident(Resident& r, F fn, int threads, size_t smem, int* ctas) {
+  int dev = 0;
+  if (!cuda_ok(cudaGetDevice(&dev)) || dev >= kMaxDevices) return false;
+  std::lock_guard<std::mutex> lk(r.mu);
+  if (r.ctas[dev] == 0) {
+    int sms = 0, per = 0;
+    if (!cuda_ok(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) ||
+        !cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, smem)) ||
+        !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
+      return false;
+    r.ctas[dev] = std::max(1, per) * sms;
+  }
+  *ctas = r.ctas[dev];
+  return true;
+}
+
 struct FwdLaunch {
-  template <typename X, typename Z, typename O, int GATE, int V>
-  static void go(const GatedParams& p, const GatedPlan& pl, cudaStream_t st) {
-    gated_fwd<X, Z, O, GATE, V, kGatedJ, kGatedNW><<<(unsigned)pl.tiles, 32 * pl.NW, 0, st>>>(p);
+  template <typename X, typename Z, typename O, int GATE>
+  static wkv_status go(const GatedParams& p, const GatedPlan& pl, cudaStream_t st) {
+    static Resident r;
+    const auto fn = gated_fwd<X, Z, O, GATE, kGatedJ, kGatedNW>;
+    int ctas;
+    if (!resident(r, fn, 32 * kGatedNW, gated_fwd_smem<X, Z, kGatedJ, kGatedNW>(), &ctas)) return WKV_ERR_CUDA;
+    // a single tile of fewer warps takes less shared memory: more CTAs fit
+    const size_t smem = gated_fwd_smem<X, Z, kGatedJ, kGatedNW>() / kGatedNW * pl.NW;
+    const long long most = (long long)ctas * (kGatedNW / pl.NW);
+    fn<<<(unsigned)std::min(pl.tiles, most), 32 * pl.NW, smem, st>>>(p);
+    return launch_result();
   }
 };
 struct BwdLaunch {
-  template <typename X, typename Z, typename O, int GATE, int V>
-  static void go(const GatedParams& p, const GatedPlan& pl, cudaStream_t st) {
-    gated_bwd<X, Z, O, GATE, V, kGatedJ, kGatedNW><<<(unsigned)pl.tiles, 32 * pl.NW, 0, st>>>(p);
+  template <typename X, typename Z, typename O, int GATE>
+  static wkv_status go(const GatedParams& p, const GatedPlan& pl, cudaStream_t st) {
+    static Resident r;
+    const auto fn = gated_bwd<X, Z, O, GATE, kGatedJ, kGatedNW>;
+    using Smem = GatedBwdSmem<X, Z, O, kGatedJ, kGatedNW>;
+    int ctas;
+    if (!resident(r, fn, 32 * kGatedNW, Smem::kBytes, &ctas)) return WKV_ERR_CUDA;
+    const size_t smem = Smem::kBytes / kGatedNW * pl.NW;
+    const long long most = (long long)ctas * (kGatedNW / pl.NW);
+    fn<<<(unsigned)std::min(pl.tiles, most), 32 * pl.NW, smem, st>>>(p);
+    return launch_result();
   }
 };
 
 template <typename F, typename X, typename Z, typename O>
 wkv_status by_gate(int gate, const GatedParams& p, const GatedPlan& pl, cudaStream_t st) {
-  if (gate == WKV_GATE_SIGMOID) {
-    if (pl.V == 2) F::template go<X, Z, O, kGateSigmoid, 2>(p, pl, st);
-    else F::template go<X, Z, O, kGateSigmoid, 1>(p, pl, st);
-  } else {
-    if (pl.V == 2) F::template go<X, Z, O, kGateDecay, 2>(p, pl, st);
-    else F::template go<X, Z, O, kGateDecay, 1>(p, pl, st);
-  }
-  return launch_result();
+  return gate == WKV_GATE_SIGMOID ? F::template go<X, Z, O, kGateSigmoid>(p, pl, st)
+                                  : F::template go<X, Z, O, kGateDecay>(p, pl, st);
 }
 
 template <typename F>
@@ -127,18 +169,18 @@ void chain(GatedParams* p, const GatedPlan& pl, void* workspace) {
   p->nch = pl.nch;
   p->G = pl.G;
   p->ngrp = pl.ngrp;
+  p->tiles = pl.tiles;
   p->hdr = reinterpret_cast<WsHeader*>(ws);
   p->tot = reinterpret_cast<GatedRec*>(ws + pl.off_tot);
   p->pre = reinterpret_cast<GatedRec*>(ws + pl.off_pre);
   p->timeout_ns = kDefaultTimeoutNs;
 }
 
-// What forward and backward check alike; pl is filled for the vector width
-// that the call's pointers allow.
+// What forward and backward check alike.
 wkv_status check_common(int64_t B, int64_t T, int64_t C, const void* x, int x_dtype, int64_t x_sb, int64_t x_st,
                         const void* z, int z_dtype, int64_t z_sb, int64_t z_st, int gate, int o_dtype) {
   GatedPlan pl;
-  if (!gated_plan(B, T, C, 1, &pl)) return WKV_ERR_INVALID_ARG;
+  if (!gated_plan(B, T, C, &pl)) return WKV_ERR_INVALID_ARG;
   if (!types_ok(x_dtype, z_dtype, o_dtype)) return WKV_ERR_UNSUPPORTED_DTYPE;
   if (gate != WKV_GATE_SIGMOID && gate != WKV_GATE_DECAY) return WKV_ERR_INVALID_ARG;
   if (x_sb < 0 || x_st < 0 || z_sb < 0 || z_st < 0) return WKV_ERR_INVALID_ARG;
@@ -170,9 +212,8 @@ using namespace wkv;
 extern "C" {
 
 size_t wkv_gated_workspace_size(int64_t B, int64_t T, int64_t C) {
-  GatedPlan a, b;  // whichever vector width a call's pointers allow
-  if (!gated_plan(B, T, C, 1, &a) || !gated_plan(B, T, C, 2, &b)) return 0;
-  return std::max(a.bytes, b.bytes);
+  GatedPlan pl;
+  return gated_plan(B, T, C, &pl) ? pl.bytes : 0;
 }
 
 wkv_status wkv_gated_forward(int64_t B, int64_t T, int64_t C, const void* x, wkv_dtype x_dtype, int64_t x_batch_stride,
@@ -184,10 +225,8 @@ wkv_status wkv_gated_forward(int64_t B, int64_t T, int64_t C, const void* x, wkv
                                       z_token_stride, gate, out_dtype);
   if (chk != WKV_OK) return chk;
   if (out && !aligned(out, elem(out_dtype))) return WKV_ERR_MISALIGNED;
-  const bool v2 = C % 2 == 0 && vec_ok(x, x_dtype, 2, x_batch_stride, x_token_stride) &&
-                  vec_ok(z, z_dtype, 2, z_batch_stride, z_token_stride) && vec_ok(out, out_dtype, 2);
   GatedPlan pl;
-  if (!gated_plan(B, T, C, v2 ? 2 : 1, &pl)) return WKV_ERR_INVALID_ARG;
+  if (!gated_plan(B, T, C, &pl)) return WKV_ERR_INVALID_ARG;
   const wkv_status wchk = check_workspace(pl, workspace, workspace_bytes);
   if (wchk != WKV_OK) return wchk;
   if (B == 0 || C == 0) return WKV_OK;
@@ -208,6 +247,9 @@ wkv_status wkv_gated_forward(int64_t B, int64_t T, int64_t C, const void* x, wkv
   p.marks = checkpoints;
   p.out = out;
   p.h_out = state_out;
+  p.x_gran = granule(x, x_dtype, C, x_batch_stride, x_token_stride);
+  p.z_gran = granule(z, z_dtype, C, z_batch_stride, z_token_stride);
+  p.pair = C % 2 == 0 && vec_ok(out, out_dtype, 2);
   chain(&p, pl, workspace);
   return by_type<FwdLaunch>(x_dtype, z_dtype, out_dtype, gate, p, pl, st);
 }
@@ -224,11 +266,8 @@ wkv_status wkv_gated_backward(int64_t B, int64_t T, int64_t C, const void* x, wk
   if (any && (!gout || !dx || !dz)) return WKV_ERR_INVALID_ARG;
   if (any && (!aligned(gout, elem(g_dtype)) || !aligned(dx, elem(x_dtype)) || !aligned(dz, elem(z_dtype))))
     return WKV_ERR_MISALIGNED;
-  const bool v2 = C % 2 == 0 && vec_ok(x, x_dtype, 2, x_batch_stride, x_token_stride) &&
-                  vec_ok(z, z_dtype, 2, z_batch_stride, z_token_stride) && vec_ok(gout, g_dtype, 2) &&
-                  vec_ok(dx, x_dtype, 2) && vec_ok(dz, z_dtype, 2);
   GatedPlan pl;
-  if (!gated_plan(B, T, C, v2 ? 2 : 1, &pl)) return WKV_ERR_INVALID_ARG;
+  if (!gated_plan(B, T, C, &pl)) return WKV_ERR_INVALID_ARG;
   if (any && pl.nch > 1 && !checkpoints) return WKV_ERR_INVALID_ARG;
   const wkv_status wchk = check_workspace(pl, workspace, workspace_bytes);
   if (wchk != WKV_OK) return wchk;
@@ -253,6 +292,10 @@ wkv_status wkv_gated_backward(int64_t B, int64_t T, int64_t C, const void* x, wk
   p.dx = dx;
   p.dz = dz;
   p.dh0 = dstate_in;
+  p.x_gran = granule(x, x_dtype, C, x_batch_stride, x_token_stride);
+  p.z_gran = granule(z, z_dtype, C, z_batch_stride, z_token_stride);
+  p.g_gran = granule(gout, g_dtype, C, 0, 0);
+  p.pair = C % 2 == 0 && vec_ok(dx, x_dtype, 2) && vec_ok(dz, z_dtype, 2);
   chain(&p, pl, workspace);
   return by_type<BwdLaunch>(x_dtype, z_dtype, g_dtype, gate, p, pl, st);
 }

@@ -9,25 +9,28 @@
 // h -> P h + H (P the product of its f, H its own result from an empty state),
 // and spans compose: (P2, H2) after (P1, H1) is (P2 P1, P2 H1 + H2).
 //
-//   CTA    a tile: 32 lanes x V channels by NW warps x J tokens. Every thread
-//          loads its J tokens x V channels at once into registers (the loads
-//          of a whole tile are in flight together), folds them into (P, H),
-//          and the warps exchange theirs through shared memory.
+//   CTA    persistent; takes tiles of 64 channels (2 adjacent ones per lane)
+//          by NW warps x J tokens. Each warp copies its own J x 64 inputs to
+//          shared memory asynchronously, one tile ahead, folds them into
+//          (P, H), and the warps exchange theirs through shared memory.
 //   chain  tiles of one channel group hand the state on through the
 //          workspace. Tiles are numbered by a ticket with the position in the
-//          sequence slowest, so a tile waits only for tiles that have already
-//          started. Tiles form groups of G: a tile reads the state after the
-//          group before its own (one record) and the totals of the tiles
-//          before it in its group, so the sequence is walked in T/(L G) hops
-//          and every sum has one fixed order.
+//          sequence slowest and every CTA works through its tickets in order,
+//          so the tile with the smallest unfinished ticket never waits. Tiles
+//          form groups of G: a tile reads the state after the group before
+//          its own (one record) and the totals of the tiles before it in its
+//          group, so the sequence is walked in T/(L G) hops and every sum has
+//          one fixed order.
 //   replay with the state in front of its span, each warp runs its tokens
 //          again from registers and stores. Inputs are read once, outputs
 //          written once.
 // A record is 16 bytes, {P, H, tag}, moved by one 128-bit access, so its tag
-// (the launch's epoch) vouches for its data without a fence, and a reader
+// (the launch's number) vouches for its data without a fence, and a reader
 // polls the data itself.
 //
-// Bound: memory traffic (12 bytes per element fp32, 6 bf16; backward 20/10).
+// Bound: memory traffic (12 bytes per element fp32, 6 bf16; backward 20/10),
+// with instruction issue close behind: pairs of channels are computed with the
+// two-wide fp32 instructions.
 #pragma once
 
 #include "wkv_device.cuh"
@@ -37,93 +40,196 @@ namespace wkv {
 enum { kGateSigmoid = 0, kGateDecay = 1 };
 
 // ---------------------------------------------------------------------------
+// two fp32 numbers per instruction
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 splat(float a) { return make_float2(a, a); }
+// a - b as one fused operation (exact product by -1)
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, splat(-1.f), a); }
+
+// ---------------------------------------------------------------------------
 // gate arithmetic
 // ---------------------------------------------------------------------------
 // A channel that remembers thousands of tokens has 1 - f ~ 1e-4, which f in
 // fp32 holds to 2^-25 / 1e-4 = 3e-4 only, and the same error returns at every
-// token. So a gate is carried as one number c whose sign says which of f and
-// 1 - f it holds exactly to fp32:  c = -(1 - f) where 0 <= 1 - f < 1/2 (sign
-// bit set, also for 1 - f = 0), else c = f. With base = 1 or 0 accordingly,
-//     f h + b = base h + (c h + b),   f = base + c,   1 - f = (1 - base) - c,
-// and a slow gate rounds the large h once a token, not twice.
-
-// base: 1 where c holds f - 1, 0 where it holds f
-__device__ __forceinline__ float gate_base(float c) { return __float_as_int(c) < 0 ? 1.f : 0.f; }
-
-__device__ __forceinline__ float gate_pack(float m, float f) {  // m = 1 - f
-  return (m >= 0.f && m < 0.5f) ? __int_as_float(__float_as_int(m) | (int)0x80000000) : f;
+// token. So one number c is kept per gate, whose sign bit says which of 1 - f
+// and f it holds to fp32's precision:
+//     c = -(1 - f) (sign bit set, also for 1 - f = 0) near f = 1,  else c = f,
+// and with A = 1 or 0 accordingly f = A + c, 1 - f = (1 - A) - c and
+//     f h + b = A h + (c h + b),
+// which rounds the large h of a slow gate once and holds a small f relative to
+// itself (a state or gradient behind it may be large).
+__device__ __forceinline__ float gate_base(float c) {
+  return __int_as_float((__float_as_int(c) >> 31) & 0x3f800000);
 }
+__device__ __forceinline__ float2 gate_base(float2 c) { return make_float2(gate_base(c.x), gate_base(c.y)); }
+__device__ __forceinline__ float2 gate_held() { return splat(-0.f); }  // f = 1
 
 template <int GATE>
-__device__ __forceinline__ float gate_coef(float z) {
-  if constexpr (GATE == kGateSigmoid) {
-    // e^z overflows to infinity for z > 88: m = 0, the state is held, and f
-    // (then NaN) is not the number kept. z = -inf gives f = 0 exactly.
-    const float e = ex2(z * kLog2e);
-    const float m = rcp(1.f + e);
-    return gate_pack(m, e * m);
+struct Gate;
+
+template <>
+struct Gate<kGateSigmoid> {
+  // m = 1 - f = 1 / (1 + e^z), f = e^z m. z = -inf gives f = 0 and m = 1
+  // exactly, z = +inf m = 0 (f is then NaN, and not the number kept).
+  __device__ __forceinline__ static float2 coef(float2 z) {
+    const float2 t = mul2(z, splat(kLog2e));
+    const float2 e = make_float2(ex2(t.x), ex2(t.y));
+    const float2 d = add2(e, splat(1.f));
+    const float2 m = make_float2(rcp(d.x), rcp(d.y));
+    const float2 f = mul2(e, m);
+    return make_float2(m.x < 0.5f ? -m.x : f.x, m.y < 0.5f ? -m.y : f.y);
+  }
+  // i_t times x
+  __device__ __forceinline__ static float2 input(float2 A, float2 c, float2 x) {
+    return mul2(sub2(sub2(splat(1.f), A), c), x);
+  }
+  // dz_t / D_t
+  __device__ __forceinline__ static float2 slope(float2 A, float2 c, float2 h, float2 x) {
+    return mul2(mul2(sub2(h, x), add2(A, c)), sub2(sub2(splat(1.f), A), c));
+  }
+};
+
+template <>
+struct Gate<kGateDecay> {
+  // 1 - e^{-z} by its series for 0 <= z < 1/8 (first term left out z^6 / 720 <
+  // 2^-24 z), where the difference would cancel.
+  __device__ __forceinline__ static float pick(float z, float m, float f) {
+    return z >= 0.f && z < 0.125f ? -fabsf(m) : f;  // -|m|: the sign bit also for z = +-0
+  }
+  __device__ __forceinline__ static float2 coef(float2 z) {
+    const float2 t = mul2(z, splat(-kLog2e));
+    float2 m = fma2(z, splat(1.f / 120), splat(-1.f / 24));
+    m = fma2(z, m, splat(1.f / 6));
+    m = fma2(z, m, splat(-1.f / 2));
+    m = mul2(z, fma2(z, m, splat(1.f)));
+    return make_float2(pick(z.x, m.x, ex2(t.x)), pick(z.y, m.y, ex2(t.y)));
+  }
+  __device__ __forceinline__ static float2 input(float2, float2, float2 x) { return x; }
+  __device__ __forceinline__ static float2 slope(float2 A, float2 c, float2 h, float2) {
+    return mul2(mul2(h, splat(-1.f)), add2(A, c));
+  }
+};
+
+// Keeps the compiler from carrying what it derived from these numbers across
+// this point (A of a whole span beside c would not fit in registers).
+template <int J>
+__device__ __forceinline__ void forget(float2 (&c)[J]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) asm volatile("" : "+f"(c[j].x), "+f"(c[j].y));
+}
+
+// f h + b and f h
+__device__ __forceinline__ float2 gate_step(float2 A, float2 c, float2 h, float2 b) { return fma2(A, h, fma2(c, h, b)); }
+__device__ __forceinline__ float2 gate_mul(float2 A, float2 c, float2 h) { return fma2(A, h, mul2(c, h)); }
+
+// ---------------------------------------------------------------------------
+// tiles in shared memory
+// ---------------------------------------------------------------------------
+constexpr int kGatedCG = 64;  // channels per tile: 32 lanes x 2
+
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  float2 r;
+  unpack_bf16x2(*reinterpret_cast<const uint32_t*>(p), r.x, r.y);
+  return r;
+}
+// Two adjacent channels; `pair`: the address takes them as one access, else
+// one by one, the second only if it exists.
+__device__ __forceinline__ void store2(float* p, float2 v, bool pair, bool second) {
+  if (pair) {
+    *reinterpret_cast<float2*>(p) = v;
   } else {
-    const float f = ex2(-z * kLog2e);
-    // 1 - e^{-z} by its series below 1/4, where the difference would cancel
-    // (first term left out: z^7 / 7! < 2^-25 z)
-    const float s = z * (1.f - z * (1.f / 2) * (1.f - z * (1.f / 3) * (1.f - z * (1.f / 4) * (1.f - z * (1.f / 5) * (1.f - z * (1.f / 6))))));
-    return gate_pack(fabsf(z) < 0.25f ? s : 1.f - f, f);
+    p[0] = v.x;
+    if (second) p[1] = v.y;
+  }
+}
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v, bool pair, bool second) {
+  if (pair) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
+  } else {
+    p[0] = __float2bfloat16_rn(v.x);
+    if (second) p[1] = __float2bfloat16_rn(v.y);
   }
 }
 
-// f h + b
-__device__ __forceinline__ float gate_step(float c, float base, float h, float b) {
-  return fmaf(base, h, fmaf(c, h, b));
+template <int GR>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool real) {
+  // bytes beyond the source size are filled with zeros
+  const int n = real ? GR : 0;
+  if constexpr (GR == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(GR), "r"(n)
+                 : "memory");
+  }
 }
-// f p
-__device__ __forceinline__ float gate_mul(float c, float base, float p) { return fmaf(base, p, c * p); }
-// what the token adds to the state, i_t x_t
-template <int GATE>
-__device__ __forceinline__ float gate_input(float c, float base, float x) {
-  return GATE == kGateSigmoid ? ((1.f - base) - c) * x : x;
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <typename T, int J, int GR>
+__device__ __forceinline__ void copy_rows(T* dst, const T* src, long long st, int rows, int left) {
+  constexpr int kPer = GR / (int)sizeof(T);            // elements per copy
+  constexpr int kCols = kGatedCG / kPer;               // copies per row
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < J * kCols / 32; ++k) {
+    const int i = k * 32 + lane;
+    const int row = i / kCols, col = i % kCols * kPer;
+    if (row < rows) {
+      const bool real = col < left;
+      copy_async<GR>(dst + row * kGatedCG + col, real ? src + row * st + col : src, real);
+    }
+  }
 }
 
-// ---------------------------------------------------------------------------
-// V adjacent channels of one token, as they lie in memory
-// ---------------------------------------------------------------------------
-template <typename T, int V>
-struct Pack;
-template <>
-struct Pack<float, 1> {
-  float a;
-  __device__ __forceinline__ void zero() { a = 0.f; }
-  __device__ __forceinline__ void load(const float* p) { a = __ldg(p); }
-  __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = a; }
-  __device__ __forceinline__ static void store(float* p, const float (&x)[1]) { *p = x[0]; }
-};
-template <>
-struct Pack<float, 2> {
-  float2 a;
-  __device__ __forceinline__ void zero() { a = make_float2(0.f, 0.f); }
-  __device__ __forceinline__ void load(const float* p) { a = __ldg(reinterpret_cast<const float2*>(p)); }
-  __device__ __forceinline__ void get(float (&x)[2]) const { x[0] = a.x, x[1] = a.y; }
-  __device__ __forceinline__ static void store(float* p, const float (&x)[2]) {
-    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+// A warp's J rows of 64 channels into shared memory: `rows` of them, `left`
+// channels from `src` on (more are zeros). gran: bytes that base, strides and
+// row length are multiples of (16, 4, or 2: an element of bf16, copied through
+// registers).
+template <typename T, int J>
+__device__ __forceinline__ void copy_span(T* dst, const T* src, long long st, int rows, int left, int gran) {
+  if (gran == 16) {
+    copy_rows<T, J, 16>(dst, src, st, rows, left);
+  } else if (gran == 4) {
+    copy_rows<T, J, 4>(dst, src, st, rows, left);
+  } else if constexpr (sizeof(T) == 2) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = h * 32 + lane;
+      unsigned short v[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        v[j] = j < rows && col < left ? reinterpret_cast<const unsigned short*>(src)[j * st + col] : (unsigned short)0;
+#pragma unroll
+      for (int j = 0; j < J; ++j) reinterpret_cast<unsigned short*>(dst)[j * kGatedCG + col] = v[j];
+    }
   }
-};
-template <>
-struct Pack<__nv_bfloat16, 1> {
-  unsigned short a;
-  __device__ __forceinline__ void zero() { a = 0; }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const unsigned short*>(p)); }
-  __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = __uint_as_float((uint32_t)a << 16); }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&x)[1]) { *p = __float2bfloat16_rn(x[0]); }
-};
-template <>
-struct Pack<__nv_bfloat16, 2> {
-  uint32_t a;
-  __device__ __forceinline__ void zero() { a = 0; }
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldg(reinterpret_cast<const uint32_t*>(p)); }
-  __device__ __forceinline__ void get(float (&x)[2]) const { unpack_bf16x2(a, x[0], x[1]); }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&x)[2]) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x[0], x[1]);
-  }
-};
+}
 
 // ---------------------------------------------------------------------------
 // the records of the chain
@@ -154,13 +260,16 @@ constexpr uint64_t kGatedTag = 0x47415445ull << 32;  // tag = kGatedTag + the la
 
 struct GatedParams {
   int B, T, C;
-  int NG;      // channel groups of 32 V channels per batch row
+  int NG;      // channel groups of 64 per batch row
   int nch;     // tiles per sequence
   int G;       // tiles per look-back group
   int ngrp;    // look-back groups per sequence
+  long long tiles;
   const void* x;
   const void* z;
   long long x_sb, x_st, z_sb, z_st;  // element strides of the batch and token axes
+  int x_gran, z_gran, g_gran;        // copy_span's gran
+  int pair;           // whether outputs take two channels per store
   const float* h0;    // [B, C] state before the sequence, or NULL (zero)
   float* marks;       // [B, nch, C] the state in front of every tile: written by the forward (NULL: not), read by the
                       // backward
@@ -175,22 +284,28 @@ struct GatedParams {
   float* dh0;         // [B, C] or NULL
   // chain
   WsHeader* hdr;
-  GatedRec* tot;      // [items][nch][CG] totals of the tiles
-  GatedRec* pre;      // [items][ngrp][CG] state after each look-back group
+  GatedRec* tot;      // [items][nch][64] totals of the tiles
+  GatedRec* pre;      // [items][ngrp][64] state after each look-back group
   uint64_t timeout_ns;
 };
 
-// Polls one record per channel until all V carry the tag, for at most the
-// wait limit (then the status word says so and the values are whatever is
-// there: finite work follows in any case).
-template <int V>
-__device__ __forceinline__ void rec_wait(const GatedRec* r, uint64_t tag, float (&P)[V], float (&H)[V],
-                                         const GatedParams& p) {
+// Two floats of a [B, C]-like row at channel c0 (zeros past C).
+__device__ __forceinline__ float2 row_get(const float* p, long long o, int c0, int C) {
+  return make_float2(c0 < C ? p[o + c0] : 0.f, c0 + 1 < C ? p[o + c0 + 1] : 0.f);
+}
+__device__ __forceinline__ void row_put(WsHeader* hdr, float* p, long long o, int c0, int C, size_t n, float2 v) {
+  if (c0 < C && WKV_IN(hdr, o + c0, n)) p[o + c0] = v.x;
+  if (c0 + 1 < C && WKV_IN(hdr, o + c0 + 1, n)) p[o + c0 + 1] = v.y;
+}
+
+// Polls a record pair until both carry the tag, for at most the wait limit
+// (then the status word says so and the values are whatever is there: finite
+// work follows in any case).
+__device__ __forceinline__ void rec_wait(const GatedRec* r, uint64_t tag, float2& P, float2& H, const GatedParams& p) {
   uint64_t t0 = 0;
   for (int spin = 0;; ++spin) {
-    bool ok = true;
-#pragma unroll
-    for (int v = 0; v < V; ++v) ok &= rec_load(r + v, tag, P[v], H[v]);
+    bool ok = rec_load(r, tag, P.x, H.x);
+    ok &= rec_load(r + 1, tag, P.y, H.y);
     if (ok) return;
     if ((spin & 255) == 255) {
       const uint64_t now = global_ns();
@@ -202,60 +317,73 @@ __device__ __forceinline__ void rec_wait(const GatedRec* r, uint64_t tag, float 
     }
   }
 }
+__device__ __forceinline__ void rec_put(const GatedParams& p, GatedRec* r, size_t i, size_t n, float2 P, float2 H,
+                                        uint64_t tag) {
+  if (!WKV_IN(p.hdr, i + 1, n)) return;
+  rec_store(r + i, P.x, H.x, tag);
+  rec_store(r + i + 1, P.y, H.y, tag);
+}
 
-// The state in front of tile `pos` (counted along the scan's direction), for
-// one channel group, by all warps of the CTA: the record after the previous
-// look-back group (at pos = 0 `first`, the state before the sequence, which
-// tile 0's total carries on to the others), then the totals of the tiles
-// before `pos` in its own group. Shared memory: lb[NW][CG] and
-// head[CG]. Ends with every thread holding its V channels' state in h.
-template <int V>
-__device__ __forceinline__ void gated_lookback(const GatedParams& p, int item, int pos, uint64_t tag,
-                                               const float (&first)[V], float2* lb, float* head, float (&h)[V]) {
-  constexpr int CG = 32 * V;
+// h -> P h + H of one span after another
+struct Span {
+  float2 P, H;
+};
+__device__ __forceinline__ float2 apply(const Span& s, float2 h) { return fma2(s.P, h, s.H); }
+
+// The state in front of tile `pos` (counted along the scan's direction), by
+// all warps of the CTA: the record after the previous look-back group (at
+// pos = 0 `first`, the state before the sequence, which tile 0's total carries
+// on to the others), then the totals of the tiles before `pos` in its own
+// group. Has one barrier; h is the same for the lanes of every warp.
+template <int NWMAX>
+struct LookBack {
+  Span part[NWMAX][32];
+  float2 head[32];
+};
+template <int NWMAX>
+__device__ __forceinline__ float2 gated_lookback(const GatedParams& p, int item, int pos, uint64_t tag, float2 first,
+                                                 LookBack<NWMAX>& lb) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
   const int grp = pos / p.G, n = pos - grp * p.G;  // n totals to read
   const int per = (n + NW - 1) / NW;
   if (w == 0) {
-    float P[V], H[V];
-    if (grp > 0) {
-      rec_wait<V>(p.pre + ((size_t)item * p.ngrp + grp - 1) * CG + lane * V, tag, P, H, p);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) H[v] = first[v];
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) head[lane * V + v] = H[v];
+    float2 P, H = first;
+    if (grp > 0) rec_wait(p.pre + ((size_t)item * p.ngrp + grp - 1) * kGatedCG + lane * 2, tag, P, H, p);
+    lb.head[lane] = H;
   }
   if (w * per < n) {
-    float Pa[V], Ha[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) Pa[v] = 1.f, Ha[v] = 0.f;
+    Span a{splat(1.f), splat(0.f)};
     for (int i = w * per; i < min(n, (w + 1) * per); ++i) {
-      float P[V], H[V];
-      rec_wait<V>(p.tot + ((size_t)item * p.nch + grp * p.G + i) * CG + lane * V, tag, P, H, p);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        Ha[v] = fmaf(P[v], Ha[v], H[v]);
-        Pa[v] *= P[v];
-      }
+      Span s;
+      rec_wait(p.tot + ((size_t)item * p.nch + grp * p.G + i) * kGatedCG + lane * 2, tag, s.P, s.H, p);
+      a.H = apply(s, a.H);
+      a.P = mul2(a.P, s.P);
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) lb[w * CG + lane * V + v] = make_float2(Pa[v], Ha[v]);
+    lb.part[w][lane] = a;
   }
   __syncthreads();
-#pragma unroll
-  for (int v = 0; v < V; ++v) h[v] = head[lane * V + v];
-  for (int i = 0; i * per < n; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 a = lb[i * CG + lane * V + v];
-      h[v] = fmaf(a.x, h[v], a.y);
-    }
+  float2 h = lb.head[lane];
+  for (int i = 0; i * per < n; ++i) h = apply(lb.part[i][lane], h);
+  return h;
+}
+
+// The tiles of a CTA. Several tiles per sequence: by tickets, so that every
+// tile's predecessors have been taken before it. One: dealt out.
+struct Tile {
+  int pos, item, b, c0;  // position along the scan, channel group, batch row, first channel of the lane
+};
+__device__ __forceinline__ Tile gated_tile(const GatedParams& p, long long t) {
+  const int items = p.B * p.NG;
+  Tile r;
+  r.pos = (int)((uint32_t)t / (uint32_t)items);
+  r.item = (int)((uint32_t)t % (uint32_t)items);
+  r.b = r.item / p.NG;
+  r.c0 = (r.item % p.NG) * kGatedCG + (threadIdx.x & 31) * 2;
+  return r;
 }
 
 // Thread 0 counts the CTA out; the last one readies the header for the next
-// launch on this workspace.
+// launch on this workspace. (Every CTA has taken its last ticket by then.)
 __device__ __forceinline__ void gated_leave(const GatedParams& p, uint32_t epoch) {
   if (threadIdx.x == 0) {
     const uint32_t prev = atomicAdd(&p.hdr->done, 1u);
@@ -267,138 +395,132 @@ __device__ __forceinline__ void gated_leave(const GatedParams& p, uint32_t epoch
   }
 }
 
+// Shared memory of a CTA beside its input tiles.
+template <int NWMAX>
+struct GatedShared {
+  Span agg[2][NWMAX][32];   // the warps' spans, by parity of the tile
+  float2 rev[2][NWMAX][32];  // backward: their gradients (the P is the same)
+  LookBack<NWMAX> lb;
+  long long next[2];
+  uint32_t epoch;
+};
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename X, typename Z, typename O, int GATE, int V, int J, int NWMAX>
-__global__ void __launch_bounds__(32 * NWMAX) gated_fwd(const GatedParams p) {
-  constexpr int CG = 32 * V;
-  __shared__ float2 s_agg[NWMAX * CG];
-  __shared__ float2 s_lb[NWMAX * CG];
-  __shared__ float s_head[CG];
-  __shared__ uint32_t s_tick[2];
+template <typename X, typename Z, int J, int NW>
+constexpr size_t gated_fwd_smem() {
+  return (size_t)J * NW * kGatedCG * (sizeof(X) + sizeof(Z));
+}
+
+template <typename X, typename Z, typename O, int GATE, int J, int NWMAX>
+__global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const GatedParams p) {
+  using Gt = Gate<GATE>;
+  extern __shared__ __align__(16) unsigned char tiles[];
+  __shared__ GatedShared<NWMAX> sh;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
   const int L = NW * J;
-  const int items = p.B * p.NG;
-  uint32_t t = blockIdx.x, epoch = 0;
-  if (p.nch > 1) {
+  const bool chained = p.nch > 1;
+  X* sx = reinterpret_cast<X*>(tiles) + (size_t)w * J * kGatedCG;
+  Z* sz = reinterpret_cast<Z*>(tiles + (size_t)NW * J * kGatedCG * sizeof(X)) + (size_t)w * J * kGatedCG;
+
+  auto fetch = [&](long long t) {  // this warp's inputs of tile t, on their way to shared memory
+    if (t < p.tiles) {
+      const Tile a = gated_tile(p, t);
+      const int t0 = a.pos * L + w * J, c0 = a.c0 - lane * 2;
+      const int rows = min(J, p.T - t0), left = p.C - c0;
+      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, p.x_st, rows, left, p.x_gran);
+      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, p.z_st, rows, left, p.z_gran);
+    }
+    copy_commit();
+  };
+
+  long long cur = blockIdx.x;
+  uint64_t tag = 0;
+  if (chained) {
     if (threadIdx.x == 0) {
-      s_tick[0] = atomicAdd(&p.hdr->ticket, 1u);
-      s_tick[1] = *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch);
+      sh.next[0] = atomicAdd(&p.hdr->ticket, 1u);
+      sh.epoch = *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch);
     }
     __syncthreads();
-    t = s_tick[0];
-    epoch = s_tick[1];
+    cur = sh.next[0];
+    tag = kGatedTag + sh.epoch + 1u;
   }
-  const uint64_t tag = kGatedTag + epoch + 1u;
-  const int pos = (int)(t / (uint32_t)items), item = (int)(t % (uint32_t)items);
-  const int b = item / p.NG, c0 = (item % p.NG) * CG + lane * V;
-  const bool on = c0 < p.C;  // C is a multiple of V
-  const int t0 = pos * L + w * J;
+  fetch(cur);
+  for (int par = 0; cur < p.tiles; par ^= 1) {
+    const Tile a = gated_tile(p, cur);
+    const int t0 = a.pos * L + w * J;
+    const int nt = p.T - t0;  // tokens from this span on
+    long long ticket = cur + gridDim.x;
+    if (chained && threadIdx.x == 0) ticket = atomicAdd(&p.hdr->ticket, 1u);
+    // The state before the sequence enters the scan at its first tile alone:
+    // its total, which carries it on, depends on this load, so h_out may be
+    // h0. (In a single tile the barrier below stands between this load and
+    // that store.)
+    const float2 first = p.h0 && a.pos == 0 ? row_get(p.h0, (long long)a.b * p.C, a.c0, p.C) : splat(0.f);
 
-  Pack<X, V> xr[J];
-  Pack<Z, V> zr[J];
-  const X* xp = static_cast<const X*>(p.x) + b * p.x_sb + t0 * p.x_st + c0;
-  const Z* zp = static_cast<const Z*>(p.z) + b * p.z_sb + t0 * p.z_st + c0;
+    copy_wait();
+    __syncwarp();
+    Span s{splat(1.f), splat(0.f)};
+    float2 coef[J], in[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    if (on && t0 + j < p.T) {
-      xr[j].load(xp + j * p.x_st);
-      zr[j].load(zp + j * p.z_st);
+    for (int j = 0; j < J; ++j) {
+      coef[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2));
+      in[j] = Gt::input(gate_base(coef[j]), coef[j], load2(sx + j * kGatedCG + lane * 2));
     }
-  }
-  // The state before the sequence enters the scan at its first tile alone: its
-  // total, which carries it on, depends on this load, so h_out may be h0. (In
-  // a single tile the barrier below stands between this load and that store.)
-  float first[V];
+    if (nt < J) {  // tokens past the end change nothing: f = 1, nothing added
 #pragma unroll
-  for (int v = 0; v < V; ++v) first[v] = (p.h0 && on && pos == 0) ? p.h0[(size_t)b * p.C + c0 + v] : 0.f;
-
-  // fold. A token past the end changes nothing: c = -0 (f = 1), b = 0.
-  float c[J][V], in[J][V], P[V], H[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    float xf[V], zf[V];
-    xr[j].get(xf);
-    zr[j].get(zf);
-    const bool tok = on && t0 + j < p.T;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      c[j][v] = tok ? gate_coef<GATE>(zf[v]) : -0.f;
-      const float base = gate_base(c[j][v]);
-      in[j][v] = tok ? gate_input<GATE>(c[j][v], base, xf[v]) : 0.f;
-      H[v] = gate_step(c[j][v], base, H[v], in[j][v]);
-      P[v] = gate_mul(c[j][v], base, P[v]);
+      for (int j = 0; j < J; ++j)
+        if (j >= nt) coef[j] = gate_held(), in[j] = splat(0.f);
     }
-  }
 #pragma unroll
-  for (int v = 0; v < V; ++v) s_agg[w * CG + lane * V + v] = make_float2(P[v], H[v]);
-  __syncthreads();
+    for (int j = 0; j < J; ++j) {
+      const float2 A = gate_base(coef[j]);
+      s.H = gate_step(A, coef[j], s.H, in[j]);
+      s.P = gate_mul(A, coef[j], s.P);
+    }
+    sh.agg[par][w][lane] = s;
+    if (threadIdx.x == 0) sh.next[par] = ticket;
+    __syncthreads();
+    forget(coef);
+    const long long nxt = sh.next[par];
+    fetch(nxt);  // every lane's reads of the tile lie before the barrier
 
-  float h[V];
-  if (p.nch > 1) {
-    if (w == NW - 1 && pos % p.G != p.G - 1 && pos != p.nch - 1) {  // this tile's total, for the later tiles of its group
-      float Pt[V], Ht[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) Pt[v] = pos == 0 ? 0.f : 1.f, Ht[v] = first[v];
-      for (int i = 0; i < NW; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float2 a = s_agg[i * CG + lane * V + v];
-          Ht[v] = fmaf(a.x, Ht[v], a.y);
-          Pt[v] *= a.x;
+    float2 h = first;
+    if (chained) {
+      if (w == NW - 1 && a.pos % p.G != p.G - 1 && a.pos != p.nch - 1) {  // this tile's total, for the later tiles of its group
+        Span tot{splat(a.pos == 0 ? 0.f : 1.f), first};
+        for (int i = 0; i < NW; ++i) {
+          const Span u = sh.agg[par][i][lane];
+          tot.H = apply(u, tot.H);
+          tot.P = mul2(tot.P, u.P);
         }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const size_t ri = ((size_t)item * p.nch + pos) * CG + lane * V + v;
-        if (WKV_IN(p.hdr, ri, (size_t)items * p.nch * CG)) rec_store(p.tot + ri, Pt[v], Ht[v], tag);
+        rec_put(p, p.tot, ((size_t)a.item * p.nch + a.pos) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.nch * kGatedCG,
+                tot.P, tot.H, tag);
       }
+      h = gated_lookback<NWMAX>(p, a.item, a.pos, tag, first, sh.lb);
     }
-    gated_lookback<V>(p, item, pos, tag, first, s_lb, s_head, h);
-  } else {
+    if (p.marks && w == 0)
+      row_put(p.hdr, p.marks, ((long long)a.b * p.nch + a.pos) * p.C, a.c0, p.C, (size_t)p.B * p.nch * p.C, h);
+    for (int i = 0; i < w; ++i) h = apply(sh.agg[par][i][lane], h);
+    if (w == NW - 1 && a.pos % p.G == p.G - 1 && a.pos != p.nch - 1)  // the state after this look-back group
+      rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos / p.G) * kGatedCG + lane * 2,
+              (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), apply(s, h), tag);
+    // replay
+    const long long o0 = ((long long)a.b * p.T + t0) * p.C + a.c0;
+    const bool store = p.out && a.c0 < p.C;
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = first[v];
-  }
-  if (p.marks && w == 0 && on) {
-    const size_t mi = ((size_t)b * p.nch + pos) * p.C + c0;
-    if (WKV_IN(p.hdr, mi + V - 1, (size_t)p.B * p.nch * p.C)) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.marks[mi + v] = h[v];
+    for (int j = 0; j < J; ++j) {
+      h = gate_step(gate_base(coef[j]), coef[j], h, in[j]);
+      const long long o = o0 + j * (long long)p.C;
+      if (store && j < nt && WKV_IN(p.hdr, o, (size_t)p.B * p.T * p.C))
+        store2(static_cast<O*>(p.out) + o, h, p.pair, a.c0 + 1 < p.C);
     }
+    if (p.h_out && nt > 0 && nt <= J)  // this span holds the last token
+      row_put(p.hdr, p.h_out, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, h);
+    cur = nxt;
   }
-  for (int i = 0; i < w; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 a = s_agg[i * CG + lane * V + v];
-      h[v] = fmaf(a.x, h[v], a.y);
-    }
-  if (w == NW - 1 && pos % p.G == p.G - 1 && pos != p.nch - 1) {  // the state after this look-back group
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const size_t ri = ((size_t)item * p.ngrp + pos / p.G) * CG + lane * V + v;
-      if (WKV_IN(p.hdr, ri, (size_t)items * p.ngrp * CG)) rec_store(p.pre + ri, 0.f, fmaf(P[v], h[v], H[v]), tag);
-    }
-  }
-  // replay
-  O* op = static_cast<O*>(p.out) + ((size_t)b * p.T + t0) * p.C + c0;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = gate_step(c[j][v], gate_base(c[j][v]), h[v], in[j][v]);
-    if (p.out && on && t0 + j < p.T && WKV_IN(p.hdr, op + j * (size_t)p.C + V - 1 - static_cast<O*>(p.out),
-                                             (size_t)p.B * p.T * p.C))
-      Pack<O, V>::store(op + j * (size_t)p.C, h);
-  }
-  if (p.h_out && on && t0 < p.T && t0 + J >= p.T) {  // this span holds the last token
-    const size_t si = (size_t)b * p.C + c0;
-    if (WKV_IN(p.hdr, si + V - 1, (size_t)p.B * p.C)) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.h_out[si + v] = h[v];
-    }
-  }
-  if (p.nch > 1) gated_leave(p, epoch);
+  if (chained) gated_leave(p, sh.epoch);
 }
 
 // ---------------------------------------------------------------------------
@@ -407,167 +529,156 @@ __global__ void __launch_bounds__(32 * NWMAX) gated_fwd(const GatedParams p) {
 // Tiles are taken from the end of the sequence. The state in front of a tile
 // comes from the forward's marks, so only the gradient travels along the
 // chain, and the states inside the tile are computed again from x and z.
-template <typename X, typename Z, typename O, int GATE, int V, int J, int NWMAX>
-__global__ void __launch_bounds__(32 * NWMAX) gated_bwd(const GatedParams p) {
-  constexpr int CG = 32 * V;
-  __shared__ float2 s_fwd[NWMAX * CG];  // (P, H) of each warp's span
-  __shared__ float s_rev[NWMAX * CG];   // its gradient from a zero gradient behind it (the P is the same)
-  __shared__ float2 s_lb[NWMAX * CG];
-  __shared__ float s_head[CG];
-  __shared__ uint32_t s_tick[2];
+// x and z are fetched one tile ahead as soon as the states are done; g has two
+// buffers where both fit beside another CTA (kGB), else it is fetched last.
+template <typename X, typename Z, typename O, int J, int NW>
+struct GatedBwdSmem {
+  static constexpr size_t kRow = (size_t)J * NW * kGatedCG;
+  static constexpr int kGB = kRow * (sizeof(X) + sizeof(Z) + 2 * sizeof(O)) <= 88 * 1024 ? 2 : 1;
+  static constexpr size_t kBytes = kRow * (sizeof(X) + sizeof(Z) + kGB * sizeof(O));
+};
+
+template <typename X, typename Z, typename O, int GATE, int J, int NWMAX>
+__global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const GatedParams p) {
+  using Gt = Gate<GATE>;
+  constexpr int kGB = GatedBwdSmem<X, Z, O, J, NWMAX>::kGB;
+  extern __shared__ __align__(16) unsigned char tiles[];
+  __shared__ GatedShared<NWMAX> sh;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
   const int L = NW * J;
-  const int items = p.B * p.NG;
-  uint32_t t = blockIdx.x, epoch = 0;
-  if (p.nch > 1) {
+  const bool chained = p.nch > 1;
+  const size_t row = (size_t)NW * J * kGatedCG, mine = (size_t)w * J * kGatedCG;
+  X* sx = reinterpret_cast<X*>(tiles) + mine;
+  Z* sz = reinterpret_cast<Z*>(tiles + row * sizeof(X)) + mine;
+  O* sg0 = reinterpret_cast<O*>(tiles + row * (sizeof(X) + sizeof(Z))) + mine;
+
+  auto fetch_xz = [&](long long t) {
+    if (t < p.tiles) {
+      const Tile a = gated_tile(p, t);
+      const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
+      const int rows = min(J, p.T - t0), left = p.C - c0;
+      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, p.x_st, rows, left, p.x_gran);
+      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, p.z_st, rows, left, p.z_gran);
+    }
+  };
+  auto fetch_g = [&](long long t, O* dst) {
+    if (t < p.tiles) {
+      const Tile a = gated_tile(p, t);
+      const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
+      copy_span<O, J>(dst, static_cast<const O*>(p.g) + ((long long)a.b * p.T + t0) * p.C + c0, p.C, min(J, p.T - t0),
+                      p.C - c0, p.g_gran);
+    }
+  };
+
+  long long cur = blockIdx.x;
+  uint64_t tag = 0;
+  if (chained) {
     if (threadIdx.x == 0) {
-      s_tick[0] = atomicAdd(&p.hdr->ticket, 1u);
-      s_tick[1] = *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch);
+      sh.next[0] = atomicAdd(&p.hdr->ticket, 1u);
+      sh.epoch = *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch);
     }
     __syncthreads();
-    t = s_tick[0];
-    epoch = s_tick[1];
+    cur = sh.next[0];
+    tag = kGatedTag + sh.epoch + 1u;
   }
-  const uint64_t tag = kGatedTag + epoch + 1u;
-  const int pos = (int)(t / (uint32_t)items), item = (int)(t % (uint32_t)items);  // pos counts from the end
-  const int chunk = p.nch - 1 - pos;
-  const int b = item / p.NG, c0 = (item % p.NG) * CG + lane * V;
-  const bool on = c0 < p.C;
-  const int t0 = chunk * L + w * J;
+  fetch_xz(cur);
+  fetch_g(cur, sg0);
+  copy_commit();
+  for (int par = 0; cur < p.tiles; par ^= 1) {
+    const Tile a = gated_tile(p, cur);
+    const int chunk = p.nch - 1 - a.pos;  // position in the sequence
+    const int t0 = chunk * L + w * J;
+    const int nt = p.T - t0;
+    O* sg = sg0 + (kGB == 2 && par ? row : 0);
+    long long ticket = cur + gridDim.x;
+    if (chained && threadIdx.x == 0) ticket = atomicAdd(&p.hdr->ticket, 1u);
+    // gradient behind the sequence (it enters at the scan's first tile alone,
+    // as in the forward), state in front of the tile
+    const float2 first = p.dh_out && a.pos == 0 ? row_get(p.dh_out, (long long)a.b * p.C, a.c0, p.C) : splat(0.f);
+    float2 h = chained ? row_get(p.marks, ((long long)a.b * p.nch + chunk) * p.C, a.c0, p.C)
+                       : (p.h0 ? row_get(p.h0, (long long)a.b * p.C, a.c0, p.C) : splat(0.f));
 
-  Pack<X, V> xr[J];
-  Pack<Z, V> zr[J];
-  Pack<O, V> gr[J];
-  const X* xp = static_cast<const X*>(p.x) + b * p.x_sb + t0 * p.x_st + c0;
-  const Z* zp = static_cast<const Z*>(p.z) + b * p.z_sb + t0 * p.z_st + c0;
-  const size_t o0 = ((size_t)b * p.T + t0) * p.C + c0;
-  const O* gp = static_cast<const O*>(p.g) + o0;
+    copy_wait();
+    __syncwarp();
+    Span s{splat(1.f), splat(0.f)};
+    float2 coef[J], e[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    gr[j].zero();
-    if (on && t0 + j < p.T) {
-      xr[j].load(xp + j * p.x_st);
-      zr[j].load(zp + j * p.z_st);
-      gr[j].load(gp + j * (size_t)p.C);
+    for (int j = 0; j < J; ++j) {
+      coef[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2));
+      float2 x = load2(sx + j * kGatedCG + lane * 2);
+      if (j >= nt) coef[j] = gate_held(), x = splat(0.f);
+      const float2 A = gate_base(coef[j]);
+      s.H = gate_step(A, coef[j], s.H, Gt::input(A, coef[j], x));
+      s.P = gate_mul(A, coef[j], s.P);
+      if (j % 4 == 3) asm volatile("" ::: "memory");  // four tokens' loads and exponentials at a time: registers
     }
-  }
-  // gradient behind the sequence (read by the first tile of the scan alone, as
-  // in the forward), state in front of the tile
-  float first[V], h[V];
-  const float* hp = p.nch > 1 ? p.marks + ((size_t)b * p.nch + chunk) * p.C : (p.h0 ? p.h0 + (size_t)b * p.C : nullptr);
+    forget(coef);
+    float2 Q = splat(0.f);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    first[v] = (p.dh_out && on && pos == 0) ? p.dh_out[(size_t)b * p.C + c0 + v] : 0.f;
-    h[v] = (hp && on) ? hp[c0 + v] : 0.f;
-  }
-
-  float c[J][V], e[J][V], P[V], H[V], Q[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) P[v] = 1.f, H[v] = 0.f, Q[v] = 0.f;
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-    float zf[V];
-    xr[j].get(e[j]);
-    zr[j].get(zf);
-    const bool tok = on && t0 + j < p.T;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      c[j][v] = tok ? gate_coef<GATE>(zf[v]) : -0.f;
-      e[j][v] = tok ? e[j][v] : 0.f;
-      const float base = gate_base(c[j][v]);
-      H[v] = gate_step(c[j][v], base, H[v], gate_input<GATE>(c[j][v], base, e[j][v]));
-      P[v] = gate_mul(c[j][v], base, P[v]);
+    for (int j = J - 1; j >= 0; --j) {
+      float2 g = load2(sg + j * kGatedCG + lane * 2);
+      if (j >= nt) g = splat(0.f);
+      Q = gate_mul(gate_base(coef[j]), coef[j], add2(g, Q));
     }
-  }
-#pragma unroll
-  for (int j = J - 1; j >= 0; --j) {
-    float gf[V];
-    gr[j].get(gf);
-#pragma unroll
-    for (int v = 0; v < V; ++v) Q[v] = gate_mul(c[j][v], gate_base(c[j][v]), gf[v] + Q[v]);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    s_fwd[w * CG + lane * V + v] = make_float2(P[v], H[v]);
-    s_rev[w * CG + lane * V + v] = Q[v];
-  }
-  __syncthreads();
-  if (p.nch > 1 && w == 0 && pos % p.G != p.G - 1 && pos != p.nch - 1) {
-    float Pt[V], Qt[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) Pt[v] = pos == 0 ? 0.f : 1.f, Qt[v] = first[v];
-    for (int i = NW - 1; i >= 0; --i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float pi = s_fwd[i * CG + lane * V + v].x;
-        Qt[v] = fmaf(pi, Qt[v], s_rev[i * CG + lane * V + v]);
-        Pt[v] *= pi;
+    sh.agg[par][w][lane] = s;
+    sh.rev[par][w][lane] = Q;
+    if (threadIdx.x == 0) sh.next[par] = ticket;
+    __syncthreads();
+    forget(coef);
+    const long long nxt = sh.next[par];
+    if (chained && w == 0 && a.pos % p.G != p.G - 1 && a.pos != p.nch - 1) {
+      Span tot{splat(a.pos == 0 ? 0.f : 1.f), first};
+      for (int i = NW - 1; i >= 0; --i) {
+        const float2 Pi = sh.agg[par][i][lane].P;
+        tot.H = fma2(Pi, tot.H, sh.rev[par][i][lane]);
+        tot.P = mul2(tot.P, Pi);
       }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const size_t ri = ((size_t)item * p.nch + pos) * CG + lane * V + v;
-      if (WKV_IN(p.hdr, ri, (size_t)items * p.nch * CG)) rec_store(p.tot + ri, Pt[v], Qt[v], tag);
+      rec_put(p, p.tot, ((size_t)a.item * p.nch + a.pos) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.nch * kGatedCG,
+              tot.P, tot.H, tag);
     }
+    // the states of this span, and with them what D is multiplied by in dz
+    for (int i = 0; i < w; ++i) h = apply(sh.agg[par][i][lane], h);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const float2 A = gate_base(coef[j]), x = load2(sx + j * kGatedCG + lane * 2);
+      e[j] = Gt::slope(A, coef[j], h, x);
+      h = gate_step(A, coef[j], h, Gt::input(A, coef[j], x));
+    }
+    forget(coef);
+    __syncwarp();
+    fetch_xz(nxt);
+    if (kGB == 2) fetch_g(nxt, sg0 + (par ? 0 : row));
+    copy_commit();
+    float2 q = first;  // f_{t+1} D_{t+1}, what flows back into token t
+    if (chained) q = gated_lookback<NWMAX>(p, a.item, a.pos, tag, first, sh.lb);
+    for (int i = NW - 1; i > w; --i) q = fma2(sh.agg[par][i][lane].P, q, sh.rev[par][i][lane]);
+    if (w == 0 && a.pos % p.G == p.G - 1 && a.pos != p.nch - 1)
+      rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos / p.G) * kGatedCG + lane * 2,
+              (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), fma2(s.P, q, Q), tag);
+    const long long o0 = ((long long)a.b * p.T + t0) * p.C + a.c0;
+    const bool on = a.c0 < p.C, two = a.c0 + 1 < p.C;
+#pragma unroll
+    for (int j = J - 1; j >= 0; --j) {
+      const float2 A = gate_base(coef[j]);
+      float2 g = load2(sg + j * kGatedCG + lane * 2);
+      if (j >= nt) g = splat(0.f);
+      const float2 D = add2(g, q);
+      q = gate_mul(A, coef[j], D);
+      const long long o = o0 + j * (long long)p.C;
+      if (on && j < nt && WKV_IN(p.hdr, o, (size_t)p.B * p.T * p.C)) {
+        store2(static_cast<X*>(p.dx) + o, Gt::input(A, coef[j], D), p.pair, two);
+        store2(static_cast<Z*>(p.dz) + o, mul2(D, e[j]), p.pair, two);
+      }
+    }
+    if (p.dh0 && chunk == 0 && w == 0) row_put(p.hdr, p.dh0, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, q);
+    if (kGB == 1) {
+      __syncwarp();
+      fetch_g(nxt, sg0);
+      copy_commit();
+    }
+    cur = nxt;
   }
-  // the states of this span, and with them what D is multiplied by in dz
-  for (int i = 0; i < w; ++i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float2 a = s_fwd[i * CG + lane * V + v];
-      h[v] = fmaf(a.x, h[v], a.y);
-    }
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float base = gate_base(c[j][v]), f = base + c[j][v];
-      const float hn = gate_step(c[j][v], base, h[v], gate_input<GATE>(c[j][v], base, e[j][v]));
-      e[j][v] = GATE == kGateSigmoid ? (h[v] - e[j][v]) * f * ((1.f - base) - c[j][v]) : -h[v] * f;
-      h[v] = hn;
-    }
-  float q[V];  // f_{t+1} D_{t+1}, what flows back into token t
-  if (p.nch > 1) {
-    gated_lookback<V>(p, item, pos, tag, first, s_lb, s_head, q);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) q[v] = first[v];
-  }
-  for (int i = NW - 1; i > w; --i)
-#pragma unroll
-    for (int v = 0; v < V; ++v) q[v] = fmaf(s_fwd[i * CG + lane * V + v].x, q[v], s_rev[i * CG + lane * V + v]);
-  if (w == 0 && pos % p.G == p.G - 1 && pos != p.nch - 1) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const size_t ri = ((size_t)item * p.ngrp + pos / p.G) * CG + lane * V + v;
-      if (WKV_IN(p.hdr, ri, (size_t)items * p.ngrp * CG)) rec_store(p.pre + ri, 0.f, fmaf(P[v], q[v], Q[v]), tag);
-    }
-  }
-  X* dxp = static_cast<X*>(p.dx) + o0;
-  Z* dzp = static_cast<Z*>(p.dz) + o0;
-#pragma unroll
-  for (int j = J - 1; j >= 0; --j) {
-    float gf[V], dxv[V], dzv[V];
-    gr[j].get(gf);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float base = gate_base(c[j][v]), D = gf[v] + q[v];
-      dxv[v] = gate_input<GATE>(c[j][v], base, D);
-      dzv[v] = D * e[j][v];
-      q[v] = gate_mul(c[j][v], base, D);
-    }
-    if (on && t0 + j < p.T && WKV_IN(p.hdr, o0 + j * (size_t)p.C + V - 1, (size_t)p.B * p.T * p.C)) {
-      Pack<X, V>::store(dxp + j * (size_t)p.C, dxv);
-      Pack<Z, V>::store(dzp + j * (size_t)p.C, dzv);
-    }
-  }
-  if (p.dh0 && on && chunk == 0 && w == 0) {
-    const size_t si = (size_t)b * p.C + c0;
-    if (WKV_IN(p.hdr, si + V - 1, (size_t)p.B * p.C)) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.dh0[si + v] = q[v];
-    }
-  }
-  if (p.nch > 1) gated_leave(p, epoch);
+  if (chained) gated_leave(p, sh.epoch);
 }
 
 // ---------------------------------------------------------------------------
@@ -606,9 +717,12 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepParams p
   const long long o = s * p.C + (long long)cv * V;
   load_vec<float, V>(p.h_in + o, h);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const float c = gate_coef<GATE>(z[v]), base = gate_base(c);
-    h[v] = gate_step(c, base, h[v], gate_input<GATE>(c, base, x[v]));
+  for (int v = 0; v < V; v += 2) {
+    constexpr int k = V > 1 ? 1 : 0;  // V = 1: the second half of the pair repeats the first
+    const float2 c = Gate<GATE>::coef(make_float2(z[v], z[v + k])), A = gate_base(c);
+    const float2 r = gate_step(A, c, make_float2(h[v], h[v + k]), Gate<GATE>::input(A, c, make_float2(x[v], x[v + k])));
+    h[v + k] = r.y;
+    h[v] = r.x;
   }
   store_vec<float, V>(p.h_out + o, h);
   store_vec<O, V>(static_cast<O*>(p.out) + o, h);
