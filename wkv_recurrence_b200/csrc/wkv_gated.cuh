@@ -75,18 +75,17 @@ __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, spla
 // ---------------------------------------------------------------------------
 // A channel that remembers thousands of tokens has 1 - f ~ 1e-4, which f in
 // fp32 holds to 2^-25 / 1e-4 = 3e-4 only, and the same error returns at every
-// token. So one number c is kept per gate, whose sign bit says which of 1 - f
-// and f it holds to fp32's precision:
-//     c = -(1 - f) (sign bit set, also for 1 - f = 0) near f = 1,  else c = f,
+// token. So one number c is kept per gate, whose sign says which of 1 - f and f
+// it holds to fp32's precision:
+//     c = -(1 - f) < 0 near f = 1,  else c = f,
 // and with A = 1 or 0 accordingly f = A + c, 1 - f = (1 - A) - c and
 //     f h + b = A h + (c h + b),
 // which rounds the large h of a slow gate once and holds a small f relative to
-// itself (a state or gradient behind it may be large).
-__device__ __forceinline__ float gate_base(float c) {
-  return __int_as_float((__float_as_int(c) >> 31) & 0x3f800000);
-}
+// itself (a state or gradient behind it may be large). A gate of f = 1 is kept
+// as c = -1e-30, so that A is one saturated product and h stays what it is.
+constexpr float kGateHeld = -1e-30f;
+__device__ __forceinline__ float gate_base(float c) { return __saturatef(c * -1e38f); }
 __device__ __forceinline__ float2 gate_base(float2 c) { return make_float2(gate_base(c.x), gate_base(c.y)); }
-__device__ __forceinline__ float2 gate_held() { return splat(-0.f); }  // f = 1
 
 template <int GATE>
 struct Gate;
@@ -94,22 +93,26 @@ struct Gate;
 template <>
 struct Gate<kGateSigmoid> {
   // m = 1 - f = 1 / (1 + e^z), f = e^z m. z = -inf gives f = 0 and m = 1
-  // exactly, z = +inf m = 0 (f is then NaN, and not the number kept).
-  __device__ __forceinline__ static float2 coef(float2 z) {
+  // exactly, z = +inf m = 0 (f is then NaN, and not the number kept). in =
+  // i_t x.
+  __device__ __forceinline__ static float2 coef(float2 z, float2 x, float2& in) {
     const float2 t = mul2(z, splat(kLog2e));
     const float2 e = make_float2(ex2(t.x), ex2(t.y));
     const float2 d = add2(e, splat(1.f));
     const float2 m = make_float2(rcp(d.x), rcp(d.y));
-    const float2 f = mul2(e, m);
-    return make_float2(m.x < 0.5f ? -m.x : f.x, m.y < 0.5f ? -m.y : f.y);
+    const float2 f = mul2(e, m), n = fma2(m, splat(-1.f), splat(kGateHeld));
+    in = mul2(m, x);
+    return make_float2(m.x < 0.5f ? n.x : f.x, m.y < 0.5f ? n.y : f.y);
   }
-  // i_t times x
+  // i_t times x from c
   __device__ __forceinline__ static float2 input(float2 A, float2 c, float2 x) {
     return mul2(sub2(sub2(splat(1.f), A), c), x);
   }
-  // dz_t / D_t
-  __device__ __forceinline__ static float2 slope(float2 A, float2 c, float2 h, float2 x) {
-    return mul2(mul2(sub2(h, x), add2(A, c)), sub2(sub2(splat(1.f), A), c));
+  // dz_t / D_t, and i_t x
+  __device__ __forceinline__ static float2 slope(float2 A, float2 c, float2 h, float2 x, float2& in) {
+    const float2 m = sub2(sub2(splat(1.f), A), c);
+    in = mul2(m, x);
+    return mul2(mul2(sub2(h, x), add2(A, c)), m);
   }
 };
 
@@ -117,19 +120,19 @@ template <>
 struct Gate<kGateDecay> {
   // 1 - e^{-z} by its series for 0 <= z < 1/8 (first term left out z^6 / 720 <
   // 2^-24 z), where the difference would cancel.
-  __device__ __forceinline__ static float pick(float z, float m, float f) {
-    return z >= 0.f && z < 0.125f ? -fabsf(m) : f;  // -|m|: the sign bit also for z = +-0
-  }
-  __device__ __forceinline__ static float2 coef(float2 z) {
+  __device__ __forceinline__ static float2 coef(float2 z, float2 x, float2& in) {
     const float2 t = mul2(z, splat(-kLog2e));
-    float2 m = fma2(z, splat(1.f / 120), splat(-1.f / 24));
-    m = fma2(z, m, splat(1.f / 6));
-    m = fma2(z, m, splat(-1.f / 2));
-    m = mul2(z, fma2(z, m, splat(1.f)));
-    return make_float2(pick(z.x, m.x, ex2(t.x)), pick(z.y, m.y, ex2(t.y)));
+    float2 n = fma2(z, splat(-1.f / 120), splat(1.f / 24));
+    n = fma2(z, n, splat(-1.f / 6));
+    n = fma2(z, n, splat(1.f / 2));
+    n = fma2(z, n, splat(-1.f));
+    n = fma2(z, n, splat(kGateHeld));
+    in = x;
+    return make_float2(z.x >= 0.f && z.x < 0.125f ? n.x : ex2(t.x), z.y >= 0.f && z.y < 0.125f ? n.y : ex2(t.y));
   }
   __device__ __forceinline__ static float2 input(float2, float2, float2 x) { return x; }
-  __device__ __forceinline__ static float2 slope(float2 A, float2 c, float2 h, float2) {
+  __device__ __forceinline__ static float2 slope(float2 A, float2 c, float2 h, float2 x, float2& in) {
+    in = x;
     return mul2(mul2(h, splat(-1.f)), add2(A, c));
   }
 };
@@ -157,23 +160,16 @@ __device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
   unpack_bf16x2(*reinterpret_cast<const uint32_t*>(p), r.x, r.y);
   return r;
 }
-// Two adjacent channels; `pair`: the address takes them as one access, else
-// one by one, the second only if it exists.
-__device__ __forceinline__ void store2(float* p, float2 v, bool pair, bool second) {
-  if (pair) {
-    *reinterpret_cast<float2*>(p) = v;
-  } else {
-    p[0] = v.x;
-    if (second) p[1] = v.y;
-  }
+// Two adjacent channels, as one access or, where the address does not take
+// that, one by one, the second only if it exists.
+__device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
 }
-__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v, bool pair, bool second) {
-  if (pair) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
-  } else {
-    p[0] = __float2bfloat16_rn(v.x);
-    if (second) p[1] = __float2bfloat16_rn(v.y);
-  }
+template <typename T>
+__device__ __forceinline__ void store_one(T* p, float2 v, bool second) {
+  p[0] = Elem<T>::from_f32(v.x);
+  if (second) p[1] = Elem<T>::from_f32(v.y);
 }
 
 template <int GR>
@@ -191,7 +187,7 @@ __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_gr
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 template <typename T, int J, int GR>
-__device__ __forceinline__ void copy_rows(T* dst, const T* src, long long st, int rows, int left) {
+__device__ __forceinline__ void copy_rows(T* dst, const T* src, const T* safe, long long st, int rows, int left) {
   constexpr int kPer = GR / (int)sizeof(T);            // elements per copy
   constexpr int kCols = kGatedCG / kPer;               // copies per row
   const int lane = threadIdx.x & 31;
@@ -199,23 +195,22 @@ __device__ __forceinline__ void copy_rows(T* dst, const T* src, long long st, in
   for (int k = 0; k < J * kCols / 32; ++k) {
     const int i = k * 32 + lane;
     const int row = i / kCols, col = i % kCols * kPer;
-    if (row < rows) {
-      const bool real = col < left;
-      copy_async<GR>(dst + row * kGatedCG + col, real ? src + row * st + col : src, real);
-    }
+    const bool real = row < rows && col < left;
+    copy_async<GR>(dst + row * kGatedCG + col, real ? src + row * st + col : safe, real);
   }
 }
 
-// A warp's J rows of 64 channels into shared memory: `rows` of them, `left`
-// channels from `src` on (more are zeros). gran: bytes that base, strides and
+// A warp's J rows of 64 channels into shared memory: `rows` rows and `left`
+// channels exist from `src` on, the others are zeros (`safe`: an address for
+// copies of nothing). gran: bytes that base, strides and
 // row length are multiples of (16, 4, or 2: an element of bf16, copied through
 // registers).
 template <typename T, int J>
-__device__ __forceinline__ void copy_span(T* dst, const T* src, long long st, int rows, int left, int gran) {
+__device__ __forceinline__ void copy_span(T* dst, const T* src, const T* safe, long long st, int rows, int left, int gran) {
   if (gran == 16) {
-    copy_rows<T, J, 16>(dst, src, st, rows, left);
+    copy_rows<T, J, 16>(dst, src, safe, st, rows, left);
   } else if (gran == 4) {
-    copy_rows<T, J, 4>(dst, src, st, rows, left);
+    copy_rows<T, J, 4>(dst, src, safe, st, rows, left);
   } else if constexpr (sizeof(T) == 2) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -429,8 +424,10 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
       const Tile a = gated_tile(p, t);
       const int t0 = a.pos * L + w * J, c0 = a.c0 - lane * 2;
       const int rows = min(J, p.T - t0), left = p.C - c0;
-      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, p.x_st, rows, left, p.x_gran);
-      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, p.z_st, rows, left, p.z_gran);
+      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, static_cast<const X*>(p.x), p.x_st,
+                      rows, left, p.x_gran);
+      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, static_cast<const Z*>(p.z), p.z_st,
+                      rows, left, p.z_gran);
     }
     copy_commit();
   };
@@ -464,14 +461,12 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     Span s{splat(1.f), splat(0.f)};
     float2 coef[J], in[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      coef[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2));
-      in[j] = Gt::input(gate_base(coef[j]), coef[j], load2(sx + j * kGatedCG + lane * 2));
-    }
-    if (nt < J) {  // tokens past the end change nothing: f = 1, nothing added
+    for (int j = 0; j < J; ++j)
+      coef[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2), load2(sx + j * kGatedCG + lane * 2), in[j]);
+    if (nt < J) {  // tokens past the end (their x is 0) change nothing: f = 1
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (j >= nt) coef[j] = gate_held(), in[j] = splat(0.f);
+        if (j >= nt) coef[j] = splat(kGateHeld);
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -507,14 +502,23 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
       rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos / p.G) * kGatedCG + lane * 2,
               (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), apply(s, h), tag);
     // replay
-    const long long o0 = ((long long)a.b * p.T + t0) * p.C + a.c0;
+    O* op = static_cast<O*>(p.out) + ((long long)a.b * p.T + t0) * p.C + a.c0;
     const bool store = p.out && a.c0 < p.C;
+    if (nt >= J && p.pair) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      h = gate_step(gate_base(coef[j]), coef[j], h, in[j]);
-      const long long o = o0 + j * (long long)p.C;
-      if (store && j < nt && WKV_IN(p.hdr, o, (size_t)p.B * p.T * p.C))
-        store2(static_cast<O*>(p.out) + o, h, p.pair, a.c0 + 1 < p.C);
+      for (int j = 0; j < J; ++j) {
+        h = gate_step(gate_base(coef[j]), coef[j], h, in[j]);
+        if (store && WKV_IN(p.hdr, op + 1 - static_cast<O*>(p.out), (size_t)p.B * p.T * p.C)) store2(op, h);
+        op += p.C;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        h = gate_step(gate_base(coef[j]), coef[j], h, in[j]);
+        if (store && j < nt && WKV_IN(p.hdr, op - static_cast<O*>(p.out), (size_t)p.B * p.T * p.C))
+          store_one(op, h, a.c0 + 1 < p.C);
+        op += p.C;
+      }
     }
     if (p.h_out && nt > 0 && nt <= J)  // this span holds the last token
       row_put(p.hdr, p.h_out, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, h);
@@ -557,16 +561,18 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
       const Tile a = gated_tile(p, t);
       const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
       const int rows = min(J, p.T - t0), left = p.C - c0;
-      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, p.x_st, rows, left, p.x_gran);
-      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, p.z_st, rows, left, p.z_gran);
+      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, static_cast<const X*>(p.x), p.x_st,
+                      rows, left, p.x_gran);
+      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, static_cast<const Z*>(p.z), p.z_st,
+                      rows, left, p.z_gran);
     }
   };
   auto fetch_g = [&](long long t, O* dst) {
     if (t < p.tiles) {
       const Tile a = gated_tile(p, t);
       const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
-      copy_span<O, J>(dst, static_cast<const O*>(p.g) + ((long long)a.b * p.T + t0) * p.C + c0, p.C, min(J, p.T - t0),
-                      p.C - c0, p.g_gran);
+      copy_span<O, J>(dst, static_cast<const O*>(p.g) + ((long long)a.b * p.T + t0) * p.C + c0, static_cast<const O*>(p.g),
+                      p.C, min(J, p.T - t0), p.C - c0, p.g_gran);
     }
   };
 
@@ -604,22 +610,19 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     float2 coef[J], e[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      coef[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2));
-      float2 x = load2(sx + j * kGatedCG + lane * 2);
-      if (j >= nt) coef[j] = gate_held(), x = splat(0.f);
+      float2 in;
+      coef[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2), load2(sx + j * kGatedCG + lane * 2), in);
+      if (nt < J && j >= nt) coef[j] = splat(kGateHeld);  // past the end: f = 1 (x and g are 0)
       const float2 A = gate_base(coef[j]);
-      s.H = gate_step(A, coef[j], s.H, Gt::input(A, coef[j], x));
+      s.H = gate_step(A, coef[j], s.H, in);
       s.P = gate_mul(A, coef[j], s.P);
       if (j % 4 == 3) asm volatile("" ::: "memory");  // four tokens' loads and exponentials at a time: registers
     }
     forget(coef);
     float2 Q = splat(0.f);
 #pragma unroll
-    for (int j = J - 1; j >= 0; --j) {
-      float2 g = load2(sg + j * kGatedCG + lane * 2);
-      if (j >= nt) g = splat(0.f);
-      Q = gate_mul(gate_base(coef[j]), coef[j], add2(g, Q));
-    }
+    for (int j = J - 1; j >= 0; --j)
+      Q = gate_mul(gate_base(coef[j]), coef[j], add2(load2(sg + j * kGatedCG + lane * 2), Q));
     sh.agg[par][w][lane] = s;
     sh.rev[par][w][lane] = Q;
     if (threadIdx.x == 0) sh.next[par] = ticket;
@@ -640,9 +643,10 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     for (int i = 0; i < w; ++i) h = apply(sh.agg[par][i][lane], h);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const float2 A = gate_base(coef[j]), x = load2(sx + j * kGatedCG + lane * 2);
-      e[j] = Gt::slope(A, coef[j], h, x);
-      h = gate_step(A, coef[j], h, Gt::input(A, coef[j], x));
+      const float2 A = gate_base(coef[j]);
+      float2 in;
+      e[j] = Gt::slope(A, coef[j], h, load2(sx + j * kGatedCG + lane * 2), in);
+      h = gate_step(A, coef[j], h, in);
     }
     forget(coef);
     __syncwarp();
@@ -655,19 +659,29 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     if (w == 0 && a.pos % p.G == p.G - 1 && a.pos != p.nch - 1)
       rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos / p.G) * kGatedCG + lane * 2,
               (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), fma2(s.P, q, Q), tag);
-    const long long o0 = ((long long)a.b * p.T + t0) * p.C + a.c0;
-    const bool on = a.c0 < p.C, two = a.c0 + 1 < p.C;
+    long long o = ((long long)a.b * p.T + t0 + J - 1) * p.C + a.c0;
+    const bool on = a.c0 < p.C;
+    if (nt >= J && p.pair) {
 #pragma unroll
-    for (int j = J - 1; j >= 0; --j) {
-      const float2 A = gate_base(coef[j]);
-      float2 g = load2(sg + j * kGatedCG + lane * 2);
-      if (j >= nt) g = splat(0.f);
-      const float2 D = add2(g, q);
-      q = gate_mul(A, coef[j], D);
-      const long long o = o0 + j * (long long)p.C;
-      if (on && j < nt && WKV_IN(p.hdr, o, (size_t)p.B * p.T * p.C)) {
-        store2(static_cast<X*>(p.dx) + o, Gt::input(A, coef[j], D), p.pair, two);
-        store2(static_cast<Z*>(p.dz) + o, mul2(D, e[j]), p.pair, two);
+      for (int j = J - 1; j >= 0; --j) {
+        const float2 A = gate_base(coef[j]), D = add2(load2(sg + j * kGatedCG + lane * 2), q);
+        q = gate_mul(A, coef[j], D);
+        if (on && WKV_IN(p.hdr, o + 1, (size_t)p.B * p.T * p.C)) {
+          store2(static_cast<X*>(p.dx) + o, Gt::input(A, coef[j], D));
+          store2(static_cast<Z*>(p.dz) + o, mul2(D, e[j]));
+        }
+        o -= p.C;
+      }
+    } else {
+#pragma unroll
+      for (int j = J - 1; j >= 0; --j) {
+        const float2 A = gate_base(coef[j]), D = add2(load2(sg + j * kGatedCG + lane * 2), q);
+        q = gate_mul(A, coef[j], D);
+        if (on && j < nt && WKV_IN(p.hdr, o, (size_t)p.B * p.T * p.C)) {
+          store_one(static_cast<X*>(p.dx) + o, Gt::input(A, coef[j], D), a.c0 + 1 < p.C);
+          store_one(static_cast<Z*>(p.dz) + o, mul2(D, e[j]), a.c0 + 1 < p.C);
+        }
+        o -= p.C;
       }
     }
     if (p.dh0 && chunk == 0 && w == 0) row_put(p.hdr, p.dh0, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, q);
@@ -719,8 +733,9 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepParams p
 #pragma unroll
   for (int v = 0; v < V; v += 2) {
     constexpr int k = V > 1 ? 1 : 0;  // V = 1: the second half of the pair repeats the first
-    const float2 c = Gate<GATE>::coef(make_float2(z[v], z[v + k])), A = gate_base(c);
-    const float2 r = gate_step(A, c, make_float2(h[v], h[v + k]), Gate<GATE>::input(A, c, make_float2(x[v], x[v + k])));
+    float2 in;
+    const float2 c = Gate<GATE>::coef(make_float2(z[v], z[v + k]), make_float2(x[v], x[v + k]), in);
+    const float2 r = gate_step(gate_base(c), c, make_float2(h[v], h[v + k]), in);
     h[v + k] = r.y;
     h[v] = r.x;
   }
