@@ -38,10 +38,13 @@ bool gated_plan(int64_t B, int64_t T, int64_t C, GatedPlan* pl) {
   pl->NG = (int)NG;
   pl->nch = (int)nch;
   pl->NW = nch > 1 ? kGatedNW : (int)std::max<int64_t>(1, (T + kGatedJ - 1) / kGatedJ);
-  // Many channel groups: the tile before is done by the time a tile starts,
-  // and reading one state beats reading up to 15 totals. Few: the hops along
-  // the sequence are what takes time, and 16 tiles share one.
-  pl->G = items >= 512 ? 1 : 16;
+  // Tiles per look-back group. A hop from group to group takes about 2 us, in
+  // which the CTAs of a B200 finish about 256 tiles: with that many tiles to a
+  // group (over all channel groups) the hops do not limit. No more than needed:
+  // a tile reads up to G - 1 totals. One where the tile before is long done.
+  int G = 1;
+  while (G < 32 && G * items < 256) G *= 2;
+  pl->G = G;
   pl->ngrp = (int)((nch + pl->G - 1) / pl->G);
   pl->tiles = items * nch;
   size_t off = sizeof(WsHeader);

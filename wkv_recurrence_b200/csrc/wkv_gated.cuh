@@ -188,15 +188,31 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 
 template <typename T, int J, int GR>
 __device__ __forceinline__ void copy_rows(T* dst, const T* src, const T* safe, long long st, int rows, int left) {
-  constexpr int kPer = GR / (int)sizeof(T);            // elements per copy
-  constexpr int kCols = kGatedCG / kPer;               // copies per row
+  constexpr int kPer = GR / (int)sizeof(T);  // elements per copy
+  constexpr int kCols = kGatedCG / kPer;     // copies per row
   const int lane = threadIdx.x & 31;
+  if constexpr (kCols <= 32) {  // 32 / kCols rows at a time, a lane stays in its column
+    constexpr int kStep = 32 / kCols;
+    const int row = lane / kCols, col = lane % kCols * kPer;
+    const T* at = src + row * st + col;
+    T* to = dst + row * kGatedCG + col;
+    if (rows >= J && left >= kGatedCG) {
 #pragma unroll
-  for (int k = 0; k < J * kCols / 32; ++k) {
-    const int i = k * 32 + lane;
-    const int row = i / kCols, col = i % kCols * kPer;
-    const bool real = row < rows && col < left;
-    copy_async<GR>(dst + row * kGatedCG + col, real ? src + row * st + col : safe, real);
+      for (int k = 0; k < J / kStep; ++k, at += kStep * st) copy_async<GR>(to + k * kStep * kGatedCG, at, true);
+    } else {
+#pragma unroll
+      for (int k = 0; k < J / kStep; ++k, at += kStep * st) {
+        const bool real = row + k * kStep < rows && col < left;
+        copy_async<GR>(to + k * kStep * kGatedCG, real ? at : safe, real);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < J * kCols / 32; ++k) {
+      const int row = k * 32 / kCols, col = (k * 32 % kCols + lane) * kPer;
+      const bool real = row < rows && col < left;
+      copy_async<GR>(dst + row * kGatedCG + col, real ? src + row * st + col : safe, real);
+    }
   }
 }
 
@@ -213,15 +229,17 @@ __device__ __forceinline__ void copy_span(T* dst, const T* src, const T* safe, l
     copy_rows<T, J, 4>(dst, src, safe, st, rows, left);
   } else if constexpr (sizeof(T) == 2) {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i = 0; i < 2 * J; i += 8) {  // eight loads in flight: what the callers' registers leave room for
+      unsigned short v[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int col = h * 32 + lane;
-      unsigned short v[J];
+      for (int k = 0; k < 8; ++k) {
+        const int j = (i + k) >> 1, col = (k & 1) * 32 + lane;
+        v[k] = j < rows && col < left ? reinterpret_cast<const unsigned short*>(src)[j * st + col] : (unsigned short)0;
+      }
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        v[j] = j < rows && col < left ? reinterpret_cast<const unsigned short*>(src)[j * st + col] : (unsigned short)0;
-#pragma unroll
-      for (int j = 0; j < J; ++j) reinterpret_cast<unsigned short*>(dst)[j * kGatedCG + col] = v[j];
+      for (int k = 0; k < 8; ++k)
+        reinterpret_cast<unsigned short*>(dst)[((i + k) >> 1) * kGatedCG + (k & 1) * 32 + lane] = v[k];
     }
   }
 }
@@ -325,26 +343,62 @@ struct Span {
 };
 __device__ __forceinline__ float2 apply(const Span& s, float2 h) { return fma2(s.P, h, s.H); }
 
-// The state in front of tile `pos` (counted along the scan's direction), by
-// all warps of the CTA: the record after the previous look-back group (at
-// pos = 0 `first`, the state before the sequence, which tile 0's total carries
-// on to the others), then the totals of the tiles before `pos` in its own
-// group. Has one barrier; h is the same for the lanes of every warp.
-template <int NWMAX>
-struct LookBack {
-  Span part[NWMAX][32];
-  float2 head[32];
+// The state in front of tile `pos` (counted along the scan's direction) comes
+// from the record of the look-back group before it; at pos = 0 it is `first`,
+// the state before the sequence, which tile 0's total carries on to the other
+// tiles of its group.
+//
+// Groups of one tile (G = 1: many channel groups, the tile before is done):
+// every warp asks for the record when it starts the tile and has it when the
+// tile's own spans are folded.
+struct Head {
+  float2 H;
+  bool got;
 };
+__device__ __forceinline__ const GatedRec* head_rec(const GatedParams& p, int item, int pos) {
+  return p.pre + ((size_t)item * p.ngrp + pos / p.G - 1) * kGatedCG + (threadIdx.x & 31) * 2;
+}
+__device__ __forceinline__ Head head_ask(const GatedParams& p, int item, int pos, uint64_t tag, float2 first) {
+  Head r{first, true};
+  if (p.G == 1 && pos > 0) {
+    float P;
+    const GatedRec* rec = head_rec(p, item, pos);
+    const bool a = rec_load(rec, tag, P, r.H.x), b = rec_load(rec + 1, tag, P, r.H.y);
+    r.got = a && b;
+  }
+  return r;
+}
+__device__ __forceinline__ float2 head_get(const GatedParams& p, int item, int pos, uint64_t tag, Head r) {
+  if (!r.got) {
+    float2 P;
+    rec_wait(head_rec(p, item, pos), tag, P, r.H, p);
+  }
+  return r.H;
+}
+
+// Groups of several tiles: the warps gather the totals of the tiles before
+// `pos` in its group, which do not wait for the chain, and warp 0 the record.
+// The tile that ends its group is a link of the chain: there warp 0 first joins
+// all totals, its own tile's included, then waits for the record and hands the
+// state on at once, before the other warps know it (1 x 65536 x 64: 70 us
+// without this, 20 with it).
 template <int NWMAX>
-__device__ __forceinline__ float2 gated_lookback(const GatedParams& p, int item, int pos, uint64_t tag, float2 first,
-                                                 LookBack<NWMAX>& lb) {
+struct Front {
+  Span part[NWMAX][32];
+  float2 h[32];
+};
+template <int NWMAX, typename Total>
+__device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, int pos, uint64_t tag, float2 first,
+                                              Front<NWMAX>& fr, const Total& own) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
   const int grp = pos / p.G, n = pos - grp * p.G;  // n totals to read
   const int per = (n + NW - 1) / NW;
-  if (w == 0) {
-    float2 P, H = first;
-    if (grp > 0) rec_wait(p.pre + ((size_t)item * p.ngrp + grp - 1) * kGatedCG + lane * 2, tag, P, H, p);
-    lb.head[lane] = H;
+  const bool group_end = n == p.G - 1, last = pos == p.nch - 1;
+  if (w == NW - 1 && !group_end && !last) {  // this tile's total, for the later tiles of its group
+    Span tot = own();
+    if (pos == 0) tot.H = apply(tot, first), tot.P = splat(0.f);
+    rec_put(p, p.tot, ((size_t)item * p.nch + pos) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.nch * kGatedCG, tot.P,
+            tot.H, tag);
   }
   if (w * per < n) {
     Span a{splat(1.f), splat(0.f)};
@@ -354,11 +408,36 @@ __device__ __forceinline__ float2 gated_lookback(const GatedParams& p, int item,
       a.H = apply(s, a.H);
       a.P = mul2(a.P, s.P);
     }
-    lb.part[w][lane] = a;
+    fr.part[w][lane] = a;
+  }
+  const bool hand_on = group_end && !last;
+  if (w == 0 && !hand_on) {
+    float2 P, H = first;
+    if (grp > 0) rec_wait(head_rec(p, item, pos), tag, P, H, p);
+    fr.h[lane] = H;
   }
   __syncthreads();
-  float2 h = lb.head[lane];
-  for (int i = 0; i * per < n; ++i) h = apply(lb.part[i][lane], h);
+  if (hand_on) {
+    if (w == 0) {
+      Span a{splat(1.f), splat(0.f)};
+      for (int i = 0; i * per < n; ++i) {
+        const Span s = fr.part[i][lane];
+        a.H = apply(s, a.H);
+        a.P = mul2(a.P, s.P);
+      }
+      const Span tot = own();
+      a.H = apply(tot, a.H);
+      a.P = mul2(tot.P, a.P);
+      float2 P, H = first;
+      if (grp > 0) rec_wait(head_rec(p, item, pos), tag, P, H, p);
+      rec_put(p, p.pre, ((size_t)item * p.ngrp + grp) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.ngrp * kGatedCG,
+              splat(0.f), apply(a, H), tag);
+      fr.h[lane] = H;
+    }
+    __syncthreads();
+  }
+  float2 h = fr.h[lane];
+  for (int i = 0; i * per < n; ++i) h = apply(fr.part[i][lane], h);
   return h;
 }
 
@@ -395,7 +474,7 @@ template <int NWMAX>
 struct GatedShared {
   Span agg[2][NWMAX][32];   // the warps' spans, by parity of the tile
   float2 rev[2][NWMAX][32];  // backward: their gradients (the P is the same)
-  LookBack<NWMAX> lb;
+  Front<NWMAX> front;
   long long next[2];
   uint32_t epoch;
 };
@@ -419,9 +498,8 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
   X* sx = reinterpret_cast<X*>(tiles) + (size_t)w * J * kGatedCG;
   Z* sz = reinterpret_cast<Z*>(tiles + (size_t)NW * J * kGatedCG * sizeof(X)) + (size_t)w * J * kGatedCG;
 
-  auto fetch = [&](long long t) {  // this warp's inputs of tile t, on their way to shared memory
+  auto fetch = [&](long long t, const Tile& a) {  // this warp's inputs of tile t, on their way to shared memory
     if (t < p.tiles) {
-      const Tile a = gated_tile(p, t);
       const int t0 = a.pos * L + w * J, c0 = a.c0 - lane * 2;
       const int rows = min(J, p.T - t0), left = p.C - c0;
       copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, static_cast<const X*>(p.x), p.x_st,
@@ -443,9 +521,9 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     cur = sh.next[0];
     tag = kGatedTag + sh.epoch + 1u;
   }
-  fetch(cur);
+  Tile a = gated_tile(p, cur);
+  fetch(cur, a);
   for (int par = 0; cur < p.tiles; par ^= 1) {
-    const Tile a = gated_tile(p, cur);
     const int t0 = a.pos * L + w * J;
     const int nt = p.T - t0;  // tokens from this span on
     long long ticket = cur + gridDim.x;
@@ -455,6 +533,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     // h0. (In a single tile the barrier below stands between this load and
     // that store.)
     const float2 first = p.h0 && a.pos == 0 ? row_get(p.h0, (long long)a.b * p.C, a.c0, p.C) : splat(0.f);
+    const Head ask = head_ask(p, a.item, a.pos, tag, first);
 
     copy_wait();
     __syncwarp();
@@ -479,27 +558,28 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     __syncthreads();
     forget(coef);
     const long long nxt = sh.next[par];
-    fetch(nxt);  // every lane's reads of the tile lie before the barrier
+    const Tile an = gated_tile(p, nxt);
+    fetch(nxt, an);  // every lane's reads of the tile lie before the barrier
 
-    float2 h = first;
-    if (chained) {
-      if (w == NW - 1 && a.pos % p.G != p.G - 1 && a.pos != p.nch - 1) {  // this tile's total, for the later tiles of its group
-        Span tot{splat(a.pos == 0 ? 0.f : 1.f), first};
-        for (int i = 0; i < NW; ++i) {
+    float2 h;  // the state in front of the tile
+    if (chained && p.G > 1) {
+      h = gated_front<NWMAX>(p, a.item, a.pos, tag, first, sh.front, [&] {
+        Span tot = sh.agg[par][0][lane];
+        for (int i = 1; i < NW; ++i) {
           const Span u = sh.agg[par][i][lane];
           tot.H = apply(u, tot.H);
           tot.P = mul2(tot.P, u.P);
         }
-        rec_put(p, p.tot, ((size_t)a.item * p.nch + a.pos) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.nch * kGatedCG,
-                tot.P, tot.H, tag);
-      }
-      h = gated_lookback<NWMAX>(p, a.item, a.pos, tag, first, sh.lb);
+        return tot;
+      });
+    } else {
+      h = head_get(p, a.item, a.pos, tag, ask);
     }
     if (p.marks && w == 0)
       row_put(p.hdr, p.marks, ((long long)a.b * p.nch + a.pos) * p.C, a.c0, p.C, (size_t)p.B * p.nch * p.C, h);
     for (int i = 0; i < w; ++i) h = apply(sh.agg[par][i][lane], h);
-    if (w == NW - 1 && a.pos % p.G == p.G - 1 && a.pos != p.nch - 1)  // the state after this look-back group
-      rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos / p.G) * kGatedCG + lane * 2,
+    if (chained && p.G == 1 && w == NW - 1 && a.pos != p.nch - 1)  // the state after this tile
+      rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos) * kGatedCG + lane * 2,
               (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), apply(s, h), tag);
     // replay
     O* op = static_cast<O*>(p.out) + ((long long)a.b * p.T + t0) * p.C + a.c0;
@@ -523,6 +603,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     if (p.h_out && nt > 0 && nt <= J)  // this span holds the last token
       row_put(p.hdr, p.h_out, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, h);
     cur = nxt;
+    a = an;
   }
   if (chained) gated_leave(p, sh.epoch);
 }
@@ -556,9 +637,8 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
   Z* sz = reinterpret_cast<Z*>(tiles + row * sizeof(X)) + mine;
   O* sg0 = reinterpret_cast<O*>(tiles + row * (sizeof(X) + sizeof(Z))) + mine;
 
-  auto fetch_xz = [&](long long t) {
+  auto fetch_xz = [&](long long t, const Tile& a) {
     if (t < p.tiles) {
-      const Tile a = gated_tile(p, t);
       const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
       const int rows = min(J, p.T - t0), left = p.C - c0;
       copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, static_cast<const X*>(p.x), p.x_st,
@@ -567,9 +647,8 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
                       rows, left, p.z_gran);
     }
   };
-  auto fetch_g = [&](long long t, O* dst) {
+  auto fetch_g = [&](long long t, const Tile& a, O* dst) {
     if (t < p.tiles) {
-      const Tile a = gated_tile(p, t);
       const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
       copy_span<O, J>(dst, static_cast<const O*>(p.g) + ((long long)a.b * p.T + t0) * p.C + c0, static_cast<const O*>(p.g),
                       p.C, min(J, p.T - t0), p.C - c0, p.g_gran);
@@ -587,11 +666,11 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     cur = sh.next[0];
     tag = kGatedTag + sh.epoch + 1u;
   }
-  fetch_xz(cur);
-  fetch_g(cur, sg0);
+  Tile a = gated_tile(p, cur);
+  fetch_xz(cur, a);
+  fetch_g(cur, a, sg0);
   copy_commit();
   for (int par = 0; cur < p.tiles; par ^= 1) {
-    const Tile a = gated_tile(p, cur);
     const int chunk = p.nch - 1 - a.pos;  // position in the sequence
     const int t0 = chunk * L + w * J;
     const int nt = p.T - t0;
@@ -603,6 +682,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     const float2 first = p.dh_out && a.pos == 0 ? row_get(p.dh_out, (long long)a.b * p.C, a.c0, p.C) : splat(0.f);
     float2 h = chained ? row_get(p.marks, ((long long)a.b * p.nch + chunk) * p.C, a.c0, p.C)
                        : (p.h0 ? row_get(p.h0, (long long)a.b * p.C, a.c0, p.C) : splat(0.f));
+    const Head ask = head_ask(p, a.item, a.pos, tag, first);
 
     copy_wait();
     __syncwarp();
@@ -629,16 +709,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     __syncthreads();
     forget(coef);
     const long long nxt = sh.next[par];
-    if (chained && w == 0 && a.pos % p.G != p.G - 1 && a.pos != p.nch - 1) {
-      Span tot{splat(a.pos == 0 ? 0.f : 1.f), first};
-      for (int i = NW - 1; i >= 0; --i) {
-        const float2 Pi = sh.agg[par][i][lane].P;
-        tot.H = fma2(Pi, tot.H, sh.rev[par][i][lane]);
-        tot.P = mul2(tot.P, Pi);
-      }
-      rec_put(p, p.tot, ((size_t)a.item * p.nch + a.pos) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.nch * kGatedCG,
-              tot.P, tot.H, tag);
-    }
+    const Tile an = gated_tile(p, nxt);
     // the states of this span, and with them what D is multiplied by in dz
     for (int i = 0; i < w; ++i) h = apply(sh.agg[par][i][lane], h);
 #pragma unroll
@@ -650,14 +721,26 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     }
     forget(coef);
     __syncwarp();
-    fetch_xz(nxt);
-    if (kGB == 2) fetch_g(nxt, sg0 + (par ? 0 : row));
+    fetch_xz(nxt, an);
+    if (kGB == 2) fetch_g(nxt, an, sg0 + (par ? 0 : row));
     copy_commit();
-    float2 q = first;  // f_{t+1} D_{t+1}, what flows back into token t
-    if (chained) q = gated_lookback<NWMAX>(p, a.item, a.pos, tag, first, sh.lb);
+    float2 q;  // f_{t+1} D_{t+1}, what flows back into token t
+    if (chained && p.G > 1) {
+      q = gated_front<NWMAX>(p, a.item, a.pos, tag, first, sh.front, [&] {
+        Span tot{sh.agg[par][NW - 1][lane].P, sh.rev[par][NW - 1][lane]};
+        for (int i = NW - 2; i >= 0; --i) {
+          const Span u{sh.agg[par][i][lane].P, sh.rev[par][i][lane]};
+          tot.H = apply(u, tot.H);
+          tot.P = mul2(tot.P, u.P);
+        }
+        return tot;
+      });
+    } else {
+      q = head_get(p, a.item, a.pos, tag, ask);
+    }
     for (int i = NW - 1; i > w; --i) q = fma2(sh.agg[par][i][lane].P, q, sh.rev[par][i][lane]);
-    if (w == 0 && a.pos % p.G == p.G - 1 && a.pos != p.nch - 1)
-      rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos / p.G) * kGatedCG + lane * 2,
+    if (chained && p.G == 1 && w == 0 && a.pos != p.nch - 1)
+      rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos) * kGatedCG + lane * 2,
               (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), fma2(s.P, q, Q), tag);
     long long o = ((long long)a.b * p.T + t0 + J - 1) * p.C + a.c0;
     const bool on = a.c0 < p.C;
@@ -687,10 +770,11 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     if (p.dh0 && chunk == 0 && w == 0) row_put(p.hdr, p.dh0, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, q);
     if (kGB == 1) {
       __syncwarp();
-      fetch_g(nxt, sg0);
+      fetch_g(nxt, an, sg0);
       copy_commit();
     }
     cur = nxt;
+    a = an;
   }
   if (chained) gated_leave(p, sh.epoch);
 }
