@@ -59,6 +59,7 @@ def test_refusals_before_any_launch(L):
     assert bwd(L, gs=P(258)) == E.WKV_ERR_MISALIGNED
     assert L.wkv_rms_norm_backward_workspace_size(-1, 8, 1) == 0
     assert L.wkv_rms_norm_backward_workspace_size(4, 8, 3) == 0
+    assert L.wkv_rms_norm_backward_workspace_size(4, 0, 1) == 256 == L.wkv_rms_norm_backward_workspace_size(0, 0, 1)
 
 
 def test_binding_refuses_cpu_tensors_and_names_the_argument():

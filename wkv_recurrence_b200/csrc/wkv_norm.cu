@@ -8,6 +8,9 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
+#include <utility>
+#include <vector>
 
 #include "wkv_host_util.h"
 #include "wkv_norm.cuh"
@@ -28,97 +31,139 @@ bool sizes_ok(int64_t N, int64_t C, int64_t G) {
 }
 
 // Rows that start on 16 bytes.
-bool rows_ok(const void* p, int dt, int64_t stride) { return aligned(p, 16) && (stride * (int64_t)elem(dt)) % 16 == 0; }
+bool rows_ok(const void* p, int dt, int64_t stride) {
+  return aligned(p, 16) && (stride * (int64_t)elem(dt)) % 16 == 0;
+}
 
-// The team that holds a group of n8 vectors: TW lanes (0: a whole CTA of
-// `threads`) with K vectors each. K = 0: too wide for registers.
+// The team that holds a group of D columns: TW lanes (0: a whole CTA of
+// `threads`) with K vectors each, adjacent columns or (sc) strided ones. K = 0:
+// too wide for registers.
 struct Team {
   int TW, K, threads;
+  bool sc;
 };
 
-Team fwd_team(int64_t n8) {
-  if (n8 <= 32) {
+Team cta_team(int64_t n8, int K, bool sc) { return Team{0, K, (int)round_up((size_t)((n8 + K - 1) / K), 32), sc}; }
+
+Team fwd_team(int64_t D, bool vec) {
+  const int64_t n8 = (D + 7) / 8;
+  if (n8 > 4096) return Team{0, 0, 0, false};
+  if (vec && n8 <= 32) {
     // a power of two of lanes, or three vectors on a quarter as many where
     // that leaves none idle (96 columns: 4 lanes x 3 against 12 of 16 lanes)
     int tw = 4;
     while (tw < n8) tw *= 2;
-    if (n8 * 4 == 3ll * tw && tw >= 16) return Team{tw / 4, 3, 256};
-    return Team{tw, 1, 256};
+    if (n8 * 4 == 3ll * tw && tw >= 16) return Team{tw / 4, 3, 256, false};
+    return Team{tw, 1, 256, false};
   }
-  if (n8 <= 128) return Team{32, (int)((n8 + 31) / 32), 256};
-  const int K = n8 <= 1024 ? 1 : n8 <= 2048 ? 2 : 4;
-  if (n8 > 4096) return Team{0, 0, 0};
-  return Team{0, K, (int)round_up((size_t)((n8 + K - 1) / K), 32)};
+  if (vec && n8 <= 128) return Team{32, (int)((n8 + 31) / 32), 256, false};
+  return cta_team(n8, n8 <= 256 ? 1 : n8 <= 1024 ? 2 : n8 <= 2048 ? 4 : 8, !vec);
 }
 
-Team bwd_team(int64_t n8, int64_t G) {
-  Team t{0, 0, 0};
-  if (n8 <= 64) {
+Team bwd_team(int64_t D, int64_t G, bool vec) {
+  const int64_t n8 = (D + 7) / 8;
+  if (vec && n8 <= 64) {
     int tw = 4;
     while (tw < n8 && tw < 32) tw *= 2;
-    if (tw * G <= 512) return Team{tw, n8 > 32 ? 2 : 1, 0};
+    if (tw * G <= 512) return Team{tw, n8 > 32 ? 2 : 1, 0, false};
   }
-  if (G == 1 && n8 <= 2048) {
-    t.K = n8 <= 1024 ? 1 : 2;
-    t.threads = (int)round_up((size_t)((n8 + t.K - 1) / t.K), 32);
-  }
-  return t;
+  if (G == 1 && n8 <= 2048) return cta_team(n8, n8 <= 512 ? 1 : n8 <= 1024 ? 2 : 4, !vec);
+  return Team{0, 0, 0, false};
 }
 
 struct BwdPlan {
   Team team;
-  int rpc, threads, nparts;  // team kernel
-  int gparts;                // general kernels
-  size_t off_rstd, bytes;
+  int rpc, threads, nparts;
 };
 
-bool bwd_plan(int64_t N, int64_t C, int64_t G, BwdPlan* pl) {
-  if (!sizes_ok(N, C, G)) return false;
-  const int64_t D = C / G;
-  pl->team = D % 8 == 0 ? bwd_team(D / 8, G) : Team{0, 0, 0};
-  pl->nparts = 0;
-  if (pl->team.K) {
-    if (pl->team.TW) {
-      const int tpr = pl->team.TW * (int)G;
-      pl->rpc = std::max(1, 256 / tpr);
-      pl->threads = (int)round_up((size_t)pl->rpc * tpr, 32);
-    } else {
-      pl->rpc = 1;
-      pl->threads = pl->team.threads;
-    }
-    const int per_sm = std::max(1, 1024 / pl->threads);
-    pl->nparts = (int)std::max<int64_t>(1, std::min<int64_t>((N + pl->rpc - 1) / pl->rpc, (int64_t)kSms * per_sm));
+// vec: 16-byte aligned rows. Without a team (team.K = 0) the general kernels
+// run, on nparts parts of the rows.
+BwdPlan bwd_plan(int64_t N, int64_t C, int64_t G, bool vec) {
+  BwdPlan pl;
+  pl.team = bwd_team(C / G, G, vec && (C / G) % 8 == 0);
+  pl.rpc = 1;
+  pl.threads = pl.team.threads;
+  if (!pl.team.K) {
+    pl.nparts = (int)std::max<int64_t>(1, std::min<int64_t>(N, 256));
+    return pl;
   }
-  pl->gparts = (int)std::max<int64_t>(1, std::min<int64_t>(N, 256));
-  const size_t parts = (size_t)std::max(pl->nparts, pl->gparts) * (size_t)C;
-  pl->off_rstd = round_up(sizeof(float) * parts, 256);
-  pl->bytes = std::max<size_t>(256, pl->off_rstd + sizeof(float) * (size_t)(N * G));
-  return true;
+  if (pl.team.TW) {
+    const int tpr = pl.team.TW * (int)G;
+    pl.rpc = std::max(1, 256 / tpr);
+    pl.threads = (int)round_up((size_t)pl.rpc * tpr, 32);
+  }
+  // at most one wave; the launch takes as many of these as are resident
+  const int per_sm = std::max(1, 1024 / pl.threads);
+  pl.nparts = (int)std::max<int64_t>(1, std::min<int64_t>((N + pl.rpc - 1) / pl.rpc, (int64_t)kSms * per_sm));
+  return pl;
 }
 
-template <typename X, typename R, bool RES, int TW, int K>
+// [parts][C] floats, then [N][G] for the general kernels: whichever a call's
+// alignment takes.
+size_t bwd_parts_bytes(int64_t N, int64_t C, int64_t G) {
+  size_t most = 0;
+  for (const bool vec : {false, true}) most = std::max(most, (size_t)bwd_plan(N, C, G, vec).nparts);
+  return round_up(sizeof(float) * std::max<size_t>(most, 256) * (size_t)C, 256);
+}
+
+template <typename X, typename R, bool RES, int TW, int K, bool SC = false>
 void launch_team(const NormParams& p, int threads, cudaStream_t st) {
   const long long segs = p.N * p.G;
   const unsigned grid = (unsigned)(TW ? (segs * TW + 255) / 256 : segs);
-  wkv_norm_team<X, R, RES, TW, K><<<grid, threads, 0, st>>>(p);
+  wkv_norm_team<X, R, RES, TW, K, SC><<<grid, threads, 0, st>>>(p);
 }
 
 template <typename X, typename R, bool RES>
 void fwd_shape(const NormParams& p, const Team& t, cudaStream_t st) {
-  switch (t.TW * 8 + t.K) {
-    case 4 * 8 + 1: return launch_team<X, R, RES, 4, 1>(p, t.threads, st);
-    case 4 * 8 + 3: return launch_team<X, R, RES, 4, 3>(p, t.threads, st);
-    case 8 * 8 + 1: return launch_team<X, R, RES, 8, 1>(p, t.threads, st);
-    case 8 * 8 + 3: return launch_team<X, R, RES, 8, 3>(p, t.threads, st);
-    case 16 * 8 + 1: return launch_team<X, R, RES, 16, 1>(p, t.threads, st);
-    case 32 * 8 + 1: return launch_team<X, R, RES, 32, 1>(p, t.threads, st);
-    case 32 * 8 + 2: return launch_team<X, R, RES, 32, 2>(p, t.threads, st);
-    case 32 * 8 + 3: return launch_team<X, R, RES, 32, 3>(p, t.threads, st);
-    case 32 * 8 + 4: return launch_team<X, R, RES, 32, 4>(p, t.threads, st);
+  if (t.sc) {
+    switch (t.K) {
+      case 1: return launch_team<X, R, RES, 0, 1, true>(p, t.threads, st);
+      case 2: return launch_team<X, R, RES, 0, 2, true>(p, t.threads, st);
+      case 4: return launch_team<X, R, RES, 0, 4, true>(p, t.threads, st);
+      default: return launch_team<X, R, RES, 0, 8, true>(p, t.threads, st);
+    }
+  }
+  switch (t.TW * 16 + t.K) {
+    case 4 * 16 + 1: return launch_team<X, R, RES, 4, 1>(p, t.threads, st);
+    case 4 * 16 + 3: return launch_team<X, R, RES, 4, 3>(p, t.threads, st);
+    case 8 * 16 + 1: return launch_team<X, R, RES, 8, 1>(p, t.threads, st);
+    case 8 * 16 + 3: return launch_team<X, R, RES, 8, 3>(p, t.threads, st);
+    case 16 * 16 + 1: return launch_team<X, R, RES, 16, 1>(p, t.threads, st);
+    case 32 * 16 + 1: return launch_team<X, R, RES, 32, 1>(p, t.threads, st);
+    case 32 * 16 + 2: return launch_team<X, R, RES, 32, 2>(p, t.threads, st);
+    case 32 * 16 + 3: return launch_team<X, R, RES, 32, 3>(p, t.threads, st);
+    case 32 * 16 + 4: return launch_team<X, R, RES, 32, 4>(p, t.threads, st);
     case 1: return launch_team<X, R, RES, 0, 1>(p, t.threads, st);
     case 2: return launch_team<X, R, RES, 0, 2>(p, t.threads, st);
-    default: return launch_team<X, R, RES, 0, 4>(p, t.threads, st);
+    case 4: return launch_team<X, R, RES, 0, 4>(p, t.threads, st);
+    default: return launch_team<X, R, RES, 0, 8>(p, t.threads, st);
   }
+}
+
+// e4m3 scales across groups: TW lanes per group, or 0 where that kernel does
+// not fit.
+int cross_lanes(int64_t D, int64_t G) {
+  int tw = 4;
+  while (tw < D / 8) tw *= 2;
+  return tw <= 32 && tw * G <= 1024 ? tw : 0;
+}
+
+template <typename X, typename R, bool RES>
+void cross_shape(const NormParams& p, int tw, cudaStream_t st) {
+  const int tpr = tw * p.G, rpc = std::max(1, 256 / tpr);
+  const unsigned grid = (unsigned)((p.N + rpc - 1) / rpc);
+  const int threads = (int)round_up((size_t)rpc * tpr, 32);
+  const size_t smem = sizeof(int) * (size_t)rpc * p.nb;
+  if (tw == 4) wkv_norm_cross<X, R, RES, 4><<<grid, threads, smem, st>>>(p, rpc);
+  else if (tw == 8) wkv_norm_cross<X, R, RES, 8><<<grid, threads, smem, st>>>(p, rpc);
+  else if (tw == 16) wkv_norm_cross<X, R, RES, 16><<<grid, threads, smem, st>>>(p, rpc);
+  else wkv_norm_cross<X, R, RES, 32><<<grid, threads, smem, st>>>(p, rpc);
+}
+
+template <typename X, typename R, bool RES>
+void fwd_launch(const NormParams& p, const Team& t, int cross, cudaStream_t st) {
+  if (cross) cross_shape<X, R, RES>(p, cross, st);
+  else fwd_shape<X, R, RES>(p, t, st);
 }
 
 // A general row kernel may use 48 KB of shared memory without asking.
@@ -159,24 +204,33 @@ wkv_status norm(int64_t N, int64_t C, int64_t G, float eps, const void* x, int x
   p.s = res ? s : nullptr;
   p.scale = scale;
   p.block = (int)block;
+  p.nb = block ? (int)(C / block) : 0;
+  p.inv_d = 1.f / (float)p.D;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  Team t{0, 0, 0};
   const int64_t D = p.D;
-  if (D % 8 == 0 && rows_ok(x, x_dtype, x_stride) && (!res || (rows_ok(res, r_dtype, r_stride) && aligned(s, 16))) &&
-      aligned(weight, 16) && aligned(y, 16) && N * G * 32 < (1ll << 38))
-    t = fwd_team(D / 8);
-  const int width = t.TW ? t.TW : t.threads;
-  if (out_kind == kOutE4m3 && block != D && (D % block != 0 || block / 8 > width)) t.K = 0;
-  if (t.K && N * G < (1ll << 31)) {
+  const bool vec = D % 8 == 0 && rows_ok(x, x_dtype, x_stride) &&
+                   (!res || (rows_ok(res, r_dtype, r_stride) && aligned(s, 16))) && aligned(weight, 16) && aligned(y, 16);
+  Team t = fwd_team(D, vec);
+  int cross = 0;
+  if (out_kind == kOutE4m3 && block != D) {
+    const int width = t.TW ? t.TW : t.threads;
+    if (t.sc || D % block != 0 || block / 8 > width) {
+      t.K = 0;
+      cross = vec ? cross_lanes(D, G) : 0;
+    }
+  }
+  // narrow groups of rows that are not aligned: a CTA each is a waste
+  if (t.sc && t.threads < 64 && G > 1) t.K = 0;
+  if ((t.K || cross) && N * G < (1ll << 31)) {
     if (!res) {
-      if (x_dtype == WKV_F32) fwd_shape<float, float, false>(p, t, st);
-      else fwd_shape<bf, bf, false>(p, t, st);
+      if (x_dtype == WKV_F32) fwd_launch<float, float, false>(p, t, cross, st);
+      else fwd_launch<bf, bf, false>(p, t, cross, st);
     } else if (x_dtype == WKV_F32) {
-      fwd_shape<float, float, true>(p, t, st);
+      fwd_launch<float, float, true>(p, t, cross, st);
     } else if (r_dtype == WKV_F32) {
-      fwd_shape<bf, float, true>(p, t, st);
+      fwd_launch<bf, float, true>(p, t, cross, st);
     } else {
-      fwd_shape<bf, bf, true>(p, t, st);
+      fwd_launch<bf, bf, true>(p, t, cross, st);
     }
   } else {
     wkv_norm_row<<<(unsigned)N, 256, sizeof(float) * (size_t)G, st>>>(p, x_dtype == WKV_BF16, r_dtype == WKV_BF16);
@@ -184,18 +238,61 @@ wkv_status norm(int64_t N, int64_t C, int64_t G, float eps, const void* x, int x
   return launch_result();
 }
 
-template <typename Y, typename S, bool GS>
-void bwd_shape(const NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
+// CTAs of `fn` that are resident on the device at once, looked up once per
+// device and block size.
+template <typename F>
+bool resident(F fn, int threads, size_t smem, int* ctas) {
+  struct Entry {
+    int dev, threads, ctas;
+    size_t smem;
+  };
+  static std::mutex mu;  // one of each per kernel type F; fn tells kernels of one type apart
+  static std::vector<std::pair<F, Entry>> known;
+  int dev = 0;
+  if (!cuda_ok(cudaGetDevice(&dev))) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const auto& k : known)
+    if (k.first == fn && k.second.dev == dev && k.second.threads == threads && k.second.smem == smem) {
+      *ctas = k.second.ctas;
+      return true;
+    }
+  int sms = 0, per = 0;
+  if (!cuda_ok(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, fn, threads, smem)) ||
+      !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
+    return false;
+  *ctas = std::max(1, per) * sms;
+  known.push_back({fn, Entry{dev, threads, *ctas, smem}});
+  return true;
+}
+
+template <typename Y, typename S, bool GS, int TW, int K, bool SC>
+bool bwd_launch(NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
   const size_t smem = pl.rpc > 1 ? sizeof(float) * (size_t)p.C : 0;
-  const unsigned grid = (unsigned)pl.nparts;
+  int ctas;
+  if (!resident(wkv_norm_bwd_team<Y, S, GS, TW, K, SC>, pl.threads, smem, &ctas)) return false;
+  p.nparts = std::min(pl.nparts, ctas);
+  wkv_norm_bwd_team<Y, S, GS, TW, K, SC><<<(unsigned)p.nparts, pl.threads, smem, st>>>(p, pl.rpc);
+  return true;
+}
+
+template <typename Y, typename S, bool GS>
+bool bwd_shape(NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
+  if (pl.team.sc) {
+    switch (pl.team.K) {
+      case 1: return bwd_launch<Y, S, GS, 0, 1, true>(p, pl, st);
+      case 2: return bwd_launch<Y, S, GS, 0, 2, true>(p, pl, st);
+      default: return bwd_launch<Y, S, GS, 0, 4, true>(p, pl, st);
+    }
+  }
   switch (pl.team.TW * 8 + pl.team.K) {
-    case 4 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 4, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
-    case 8 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 8, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
-    case 16 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 16, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
-    case 32 * 8 + 1: wkv_norm_bwd_team<Y, S, GS, 32, 1><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
-    case 32 * 8 + 2: wkv_norm_bwd_team<Y, S, GS, 32, 2><<<grid, pl.threads, smem, st>>>(p, pl.rpc); break;
-    case 1: wkv_norm_bwd_team<Y, S, GS, 0, 1><<<grid, pl.threads, 0, st>>>(p, 1); break;
-    default: wkv_norm_bwd_team<Y, S, GS, 0, 2><<<grid, pl.threads, 0, st>>>(p, 1); break;
+    case 4 * 8 + 1: return bwd_launch<Y, S, GS, 4, 1, false>(p, pl, st);
+    case 8 * 8 + 1: return bwd_launch<Y, S, GS, 8, 1, false>(p, pl, st);
+    case 16 * 8 + 1: return bwd_launch<Y, S, GS, 16, 1, false>(p, pl, st);
+    case 32 * 8 + 1: return bwd_launch<Y, S, GS, 32, 1, false>(p, pl, st);
+    case 32 * 8 + 2: return bwd_launch<Y, S, GS, 32, 2, false>(p, pl, st);
+    case 1: return bwd_launch<Y, S, GS, 0, 1, false>(p, pl, st);
+    case 2: return bwd_launch<Y, S, GS, 0, 2, false>(p, pl, st);
+    default: return bwd_launch<Y, S, GS, 0, 4, false>(p, pl, st);
   }
 }
 
@@ -222,15 +319,15 @@ wkv_status wkv_rms_norm_quant(int64_t N, int64_t C, int64_t groups, float eps, c
 }
 
 size_t wkv_rms_norm_backward_workspace_size(int64_t N, int64_t C, int64_t groups) {
-  BwdPlan pl;
-  return bwd_plan(N, C, groups, &pl) ? pl.bytes : 0;
+  if (!sizes_ok(N, C, groups)) return 0;
+  if (C == 0) return 256;
+  return std::max<size_t>(256, bwd_parts_bytes(N, C, groups) + sizeof(float) * (size_t)(N * groups));
 }
 
 wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps, const void* gy, wkv_dtype gy_dtype,
                                  const void* sum, wkv_dtype s_dtype, int64_t s_stride, const float* weight, const void* gsum,
                                  void* dsum, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
-  BwdPlan pl;
-  if (!bwd_plan(N, C, groups, &pl)) return WKV_ERR_INVALID_ARG;
+  if (!sizes_ok(N, C, groups)) return WKV_ERR_INVALID_ARG;
   if (!(eps > 0.f) || !std::isfinite(eps)) return WKV_ERR_INVALID_ARG;
   if (!dtype_ok(gy_dtype) || !dtype_ok(s_dtype) || (gy_dtype == WKV_F32 && s_dtype != WKV_F32))
     return WKV_ERR_UNSUPPORTED_DTYPE;
@@ -240,7 +337,7 @@ wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (N == 0) return cuda_ok(cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)C, st)) ? WKV_OK : WKV_ERR_CUDA;
   if (!gy || !sum || !dsum || !workspace) return WKV_ERR_INVALID_ARG;
-  if (workspace_bytes < pl.bytes) return WKV_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < wkv_rms_norm_backward_workspace_size(N, C, groups)) return WKV_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 256) || !aligned(gy, elem(gy_dtype)) || !aligned(sum, elem(s_dtype)) ||
       !aligned(dsum, elem(s_dtype)) || (gsum && !aligned(gsum, elem(s_dtype))) || !aligned(weight, 4) || !aligned(dweight, 4))
     return WKV_ERR_MISALIGNED;
@@ -258,28 +355,29 @@ wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps
   p.gs = gsum;
   p.ds = dsum;
   p.part = static_cast<float*>(workspace);
-  p.rstd = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + pl.off_rstd);
-  const bool team = pl.team.K && aligned(gy, 16) && rows_ok(sum, s_dtype, s_stride) && (!gsum || aligned(gsum, 16)) &&
-                    aligned(dsum, 16) && aligned(weight, 16);
-  p.nparts = team ? pl.nparts : pl.gparts;
-  if (team) {
+  p.rstd = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + bwd_parts_bytes(N, C, groups));
+  p.inv_d = 1.f / (float)p.D;
+  const BwdPlan pl = bwd_plan(N, C, groups,
+                              aligned(gy, 16) && rows_ok(sum, s_dtype, s_stride) && (!gsum || aligned(gsum, 16)) &&
+                                  aligned(dsum, 16) && aligned(weight, 16));
+  p.nparts = pl.nparts;
+  if (pl.team.K) {
+    bool ok;
     if (gy_dtype == WKV_F32) {
-      if (gsum) bwd_shape<float, float, true>(p, pl, st);
-      else bwd_shape<float, float, false>(p, pl, st);
+      ok = gsum ? bwd_shape<float, float, true>(p, pl, st) : bwd_shape<float, float, false>(p, pl, st);
     } else if (s_dtype == WKV_F32) {
-      if (gsum) bwd_shape<bf, float, true>(p, pl, st);
-      else bwd_shape<bf, float, false>(p, pl, st);
+      ok = gsum ? bwd_shape<bf, float, true>(p, pl, st) : bwd_shape<bf, float, false>(p, pl, st);
     } else {
-      if (gsum) bwd_shape<bf, bf, true>(p, pl, st);
-      else bwd_shape<bf, bf, false>(p, pl, st);
+      ok = gsum ? bwd_shape<bf, bf, true>(p, pl, st) : bwd_shape<bf, bf, false>(p, pl, st);
     }
+    if (!ok) return WKV_ERR_CUDA;
   } else {
     wkv_norm_bwd_row<<<(unsigned)N, 256, 0, st>>>(p, gy_dtype == WKV_BF16, s_dtype == WKV_BF16);
     wkv_norm_bwd_cols<<<dim3((unsigned)((C + 255) / 256), (unsigned)p.nparts), 256, 0, st>>>(p, gy_dtype == WKV_BF16,
                                                                                              s_dtype == WKV_BF16);
   }
   if (launch_result() != WKV_OK) return WKV_ERR_CUDA;
-  wkv_norm_bwd_join<<<(unsigned)((C + 31) / 32), 256, 0, st>>>(p.part, p.nparts, p.C, dweight);
+  wkv_norm_bwd_join<<<(unsigned)((C + 31) / 32), 1024, 0, st>>>(p.part, p.nparts, p.C, dweight);
   return launch_result();
 }
 

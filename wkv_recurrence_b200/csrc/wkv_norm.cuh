@@ -9,8 +9,9 @@
 // y is the norm of the rounded s, the value that the stream carries on, so
 // forward and backward are about the same s.
 //
-// Bound: memory traffic; every kernel reads its inputs once into registers
-// (wkv_norm_row apart, see there) and reduces while they stay there.
+// Bound: memory traffic; the kernels read their inputs once into registers
+// (wkv_norm_row and wkv_norm_bwd_row apart, see there) and reduce while they
+// stay there.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -22,35 +23,38 @@ namespace wkv {
 constexpr float kE4m3Max = 448.f;
 constexpr int kNV = 8;  // columns per vector: 16 bytes of bf16, 32 of fp32
 
-// Eight adjacent columns as they lie in memory.
-template <typename T>
-struct Vec8;
+// Eight columns of a thread as they lie in memory: adjacent (SC false: one or
+// two 16-byte accesses), or `st` apart (SC true: element by element, adjacent
+// lanes on adjacent columns, for rows that are not 16-byte aligned), the first
+// `n` of them real.
+template <typename T, bool SC>
+struct Raw8;
 template <>
-struct Vec8<float> {
+struct Raw8<float, false> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
+  __device__ __forceinline__ void load(const float* p, int, int) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
-  __device__ __forceinline__ static void store(float* p, const float (&x)[8]) {
+  __device__ __forceinline__ static void store(float* p, int, int, const float (&x)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
 template <>
-struct Vec8<__nv_bfloat16> {
+struct Raw8<__nv_bfloat16, false> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int, int) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void get(float (&x)[8]) const {
     unpack_bf16x2(a.x, x[0], x[1]);
     unpack_bf16x2(a.y, x[2], x[3]);
     unpack_bf16x2(a.z, x[4], x[5]);
     unpack_bf16x2(a.w, x[6], x[7]);
   }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, const float (&x)[8]) {
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, int, int, const float (&x)[8]) {
     uint4 o;
     __nv_bfloat162 t;
     t = __floats2bfloat162_rn(x[0], x[1]), o.x = *reinterpret_cast<uint32_t*>(&t);
@@ -60,6 +64,40 @@ struct Vec8<__nv_bfloat16> {
     *reinterpret_cast<uint4*>(p) = o;
   }
 };
+template <typename T>
+struct Raw8<T, true> {
+  T a[8];
+  __device__ __forceinline__ void load(const T* p, int st, int n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = e < n ? p[e * st] : Elem<T>::from_f32(0.f);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = Elem<T>::to_f32(a[e]);
+  }
+  __device__ __forceinline__ static void store(T* p, int st, int n, const float (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e * st] = Elem<T>::from_f32(x[e]);
+  }
+};
+
+// The columns of vector k of team lane l, `width` lanes in the team.
+template <bool SC>
+struct Cols {
+  int at, st, n;  // first column, distance, how many of the eight exist
+  __device__ __forceinline__ Cols(int k, int l, int width, int D) {
+    at = SC ? k * kNV * width + l : (k * width + l) * kNV;
+    st = SC ? width : 1;
+    n = SC ? min(kNV, (D - at + width - 1) / width) : (at < D ? kNV : 0);
+  }
+};
+
+// (v + eps)^-1/2: the approximation and one Newton step
+__device__ __forceinline__ float inv_root(float v) {
+  const float r = rsqrtf(v);
+  return fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r);
+}
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -67,10 +105,21 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
+template <bool SC>
+__device__ __forceinline__ void store_e4m3(unsigned char* p, int st, int n, const float (&x)[8]) {
+  if constexpr (SC) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e * st] = (unsigned char)__nv_cvt_float_to_fp8(x[e], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+  }
+}
+
 // The scale of a block whose largest |y| is `top`: 1 for a block of zeros, and
 // never below the smallest normal number, so its inverse is finite.
 __device__ __forceinline__ float e4m3_scale(float top) {
-  return top > 0.f ? fmaxf(top / kE4m3Max, 1.17549435e-38f) : 1.f;
+  return top > 0.f ? fmaxf(top * (1.f / kE4m3Max), 1.17549435e-38f) : 1.f;
 }
 
 enum { kOutF32 = 0, kOutBf16 = 1, kOutE4m3 = 2 };
@@ -89,6 +138,8 @@ struct NormParams {
   void* s;              // [N, C] in the residual's type, or NULL (no residual); may be res
   float* scale;         // [N, C / block], e4m3 only
   int block;            // columns per scale, C for the whole row
+  int nb;               // C / block
+  float inv_d;          // 1 / D
 };
 
 template <int W>
@@ -127,46 +178,47 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
 // forward, one team of threads per group
 // ---------------------------------------------------------------------------
 // TW lanes (TW <= 32: several teams per warp) or the whole CTA (TW = 0) hold
-// one group's D columns in registers, K vectors of 8 per thread; vector k of
-// team lane l is columns 8 (k TW + l). Takes 16-byte aligned rows with D a
-// multiple of 8, and e4m3 scales whose block lies inside a group (the whole
-// group, or 32, 64 or 128 columns held by adjacent lanes in one k).
-template <typename X, typename R, bool RES, int TW, int K>
-__global__ void __launch_bounds__(TW ? 256 : 1024) wkv_norm_team(const NormParams p) {
+// one group's D columns in registers, K vectors of 8 per thread. Vectors of 16
+// bytes take aligned rows with D a multiple of 8; SC takes the others. e4m3
+// scales here have their block inside a group: the whole group, or 32, 64 or
+// 128 columns held by adjacent lanes in one k.
+//
+// What a row costs beside its bytes is paid per thread (index, root, scale).
+template <typename X, typename R, bool RES, int TW, int K, bool SC>
+__global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams p) {
   __shared__ float red[32];
   const int width = TW ? TW : (int)blockDim.x;
   const int tl = TW ? (int)(threadIdx.x % width) : (int)threadIdx.x;
-  const long long seg = TW ? (long long)blockIdx.x * (256 / width) + threadIdx.x / width : (long long)blockIdx.x;
-  const bool live = seg < p.N * p.G;
-  const long long row = live ? seg / p.G : 0;
-  const int g = live ? (int)(seg - row * p.G) : 0;
-  const X* xp = static_cast<const X*>(p.x) + row * p.x_st + (long long)g * p.D;
-  const R* rp = RES ? static_cast<const R*>(p.res) + row * p.res_st + (long long)g * p.D : nullptr;
-  Vec8<X> xv[K];
-  Vec8<R> rv[K];
-  bool in[K];
+  const uint32_t seg = TW ? blockIdx.x * (256 / width) + threadIdx.x / width : blockIdx.x;
+  const bool live = seg < (uint32_t)(p.N * p.G);
+  const uint32_t row = !live ? 0 : p.G == 1 ? seg : seg / (uint32_t)p.G;
+  const int gc = live ? (int)(seg - row * (uint32_t)p.G) * p.D : 0;  // the group's first column
+  const X* xp = static_cast<const X*>(p.x) + row * p.x_st + gc;
+  const R* rp = RES ? static_cast<const R*>(p.res) + row * p.res_st + gc : nullptr;
+  Raw8<X, SC> xv[K];
+  Raw8<R, SC> rv[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int col = (k * width + tl) * kNV;
-    in[k] = live && col < p.D;
-    if (in[k]) {
-      xv[k].load(xp + col);
-      if (RES) rv[k].load(rp + col);
+    const Cols<SC> c(k, tl, width, p.D);
+    if (live && c.n > 0) {
+      xv[k].load(xp + c.at, c.st, c.n);
+      if (RES) rv[k].load(rp + c.at, c.st, c.n);
     }
   }
   float s[K][kNV];
   float sum = 0.f;
-  const long long o = row * p.C + (long long)g * p.D;
+  const long long o = (long long)row * p.C + gc;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (in[k]) {
+    const Cols<SC> c(k, tl, width, p.D);
+    if (live && c.n > 0) {
       xv[k].get(s[k]);
       if (RES) {
         float r[kNV];
         rv[k].get(r);
 #pragma unroll
         for (int e = 0; e < kNV; ++e) s[k][e] = Elem<R>::to_f32(Elem<R>::from_f32(s[k][e] + r[e]));
-        Vec8<R>::store(static_cast<R*>(p.s) + o + (k * width + tl) * kNV, s[k]);
+        Raw8<R, SC>::store(static_cast<R*>(p.s) + o + c.at, c.st, c.n, s[k]);
       }
     } else {
 #pragma unroll
@@ -176,29 +228,26 @@ __global__ void __launch_bounds__(TW ? 256 : 1024) wkv_norm_team(const NormParam
     for (int e = 0; e < kNV; ++e) sum = fmaf(s[k][e], s[k][e], sum);
   }
   sum = TW ? team_sum<TW ? TW : 32>(sum) : cta_reduce<false>(sum, red);
-  const float r = 1.f / sqrtf(sum / (float)p.D + p.eps);
-  const float* wp = p.weight + (long long)g * p.D;
+  const float r = inv_root(fmaf(sum, p.inv_d, p.eps));
+  const float* wp = p.weight + gc;
+  const bool f8 = p.out_kind == kOutE4m3;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (in[k]) {
-      Vec8<float> wv;
+    const Cols<SC> c(k, tl, width, p.D);
+    if (live && c.n > 0) {
+      Raw8<float, SC> wv;
       float w[kNV];
-      wv.load(wp + (k * width + tl) * kNV);
+      wv.load(wp + c.at, c.st, c.n);
       wv.get(w);
+      // in e4m3 r joins the scale: one product less per column
 #pragma unroll
-      for (int e = 0; e < kNV; ++e) s[k][e] = s[k][e] * r * w[e];
+      for (int e = 0; e < kNV; ++e) s[k][e] = (f8 ? s[k][e] : s[k][e] * r) * w[e];
+      if (p.out_kind == kOutF32) Raw8<float, SC>::store(static_cast<float*>(p.y) + o + c.at, c.st, c.n, s[k]);
+      if (p.out_kind == kOutBf16)
+        Raw8<__nv_bfloat16, SC>::store(static_cast<__nv_bfloat16*>(p.y) + o + c.at, c.st, c.n, s[k]);
     }
   }
-  if (p.out_kind != kOutE4m3) {
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (in[k]) {
-        const long long at = o + (k * width + tl) * kNV;
-        if (p.out_kind == kOutF32) Vec8<float>::store(static_cast<float*>(p.y) + at, s[k]);
-        else Vec8<__nv_bfloat16>::store(static_cast<__nv_bfloat16*>(p.y) + at, s[k]);
-      }
-    return;
-  }
+  if (!f8) return;
   float top[K];
   float all = 0.f;
 #pragma unroll
@@ -210,20 +259,75 @@ __global__ void __launch_bounds__(TW ? 256 : 1024) wkv_norm_team(const NormParam
   }
   const bool whole = p.block == p.D;
   if (whole) all = TW ? lanes_max(all, width) : cta_reduce<true>(all, red);
-  const int per = whole ? width : p.block / kNV;  // threads that share a scale
-  const int nb = p.C / p.block;
+  const int per = p.block >> 3;  // threads that share a scale, where it is not the whole group
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const float m = whole ? all : lanes_max(top[k], per);
-    const float sc = e4m3_scale(m), inv = 1.f / sc;
-    if (in[k]) {
-      const int col = (k * width + tl) * kNV;
-      uint2 q;
-      q.x = e4m3x4(s[k][0] * inv, s[k][1] * inv, s[k][2] * inv, s[k][3] * inv);
-      q.y = e4m3x4(s[k][4] * inv, s[k][5] * inv, s[k][6] * inv, s[k][7] * inv);
-      *reinterpret_cast<uint2*>(static_cast<unsigned char*>(p.y) + o + col) = q;
-      if (tl % per == 0 && (!whole || k == 0)) p.scale[row * nb + ((long long)g * p.D + col) / p.block] = sc;
+    const Cols<SC> c(k, tl, width, p.D);
+    const float sc = e4m3_scale((whole ? all : lanes_max(top[k], per)) * r), f = r * rcp(sc);
+    if (live && c.n > 0) {
+#pragma unroll
+      for (int e = 0; e < kNV; ++e) s[k][e] *= f;
+      store_e4m3<SC>(static_cast<unsigned char*>(p.y) + o + c.at, c.st, c.n, s[k]);
+      if (whole ? k == 0 && tl == 0 : (tl & (per - 1)) == 0)
+        p.scale[(long long)row * p.nb + (whole ? (uint32_t)gc / (uint32_t)p.block : (uint32_t)(gc + c.at) / (uint32_t)p.block)] = sc;
     }
+  }
+}
+
+// e4m3 whose scale blocks reach across groups (a row of several heads, blocks
+// that straddle them): a CTA takes RPC rows, each by its groups' teams of TW
+// lanes (one vector per thread), and the blocks' maxima meet in shared memory
+// (the order of maxima does not matter).
+template <typename X, typename R, bool RES, int TW>
+__global__ void __launch_bounds__(1024) wkv_norm_cross(const NormParams p, int rpc) {
+  extern __shared__ int tops[];  // [rpc][nb]
+  const int tpr = TW * p.G;
+  const int rl = (int)threadIdx.x / tpr, tl = (int)threadIdx.x - rl * tpr;
+  const int gc = tl / TW * p.D, c = (tl % TW) * kNV;
+  const long long row = (long long)blockIdx.x * rpc + rl;
+  const bool live = rl < rpc && row < p.N && c < p.D;
+  for (int i = threadIdx.x; i < rpc * p.nb; i += blockDim.x) tops[i] = 0;
+  float s[kNV];
+  float sum = 0.f;
+  const long long o = row * p.C + gc + c;
+#pragma unroll
+  for (int e = 0; e < kNV; ++e) s[e] = 0.f;
+  if (live) {
+    Raw8<X, false> xv;
+    Raw8<R, false> rv;
+    xv.load(static_cast<const X*>(p.x) + row * p.x_st + gc + c, 1, kNV);
+    if (RES) rv.load(static_cast<const R*>(p.res) + row * p.res_st + gc + c, 1, kNV);
+    xv.get(s);
+    if (RES) {
+      float r[kNV];
+      rv.get(r);
+#pragma unroll
+      for (int e = 0; e < kNV; ++e) s[e] = Elem<R>::to_f32(Elem<R>::from_f32(s[e] + r[e]));
+      Raw8<R, false>::store(static_cast<R*>(p.s) + o, 1, kNV, s);
+    }
+#pragma unroll
+    for (int e = 0; e < kNV; ++e) sum = fmaf(s[e], s[e], sum);
+  }
+  __syncthreads();  // tops is clear
+  sum = team_sum<TW>(sum);
+  const float r = inv_root(fmaf(sum, p.inv_d, p.eps));
+  int* top = tops + rl * p.nb + (uint32_t)(gc + c) / (uint32_t)p.block;
+  if (live) {
+    Raw8<float, false> wv;
+    float w[kNV], m = 0.f;
+    wv.load(p.weight + gc + c, 1, kNV);
+    wv.get(w);
+#pragma unroll
+    for (int e = 0; e < kNV; ++e) s[e] = s[e] * r * w[e], m = fmaxf(m, fabsf(s[e]));
+    atomicMax(top, __float_as_int(m));  // bits of floats >= 0 are ordered as they are
+  }
+  __syncthreads();
+  if (live) {
+    const float sc = e4m3_scale(__int_as_float(*top)), f = rcp(sc);
+#pragma unroll
+    for (int e = 0; e < kNV; ++e) s[e] *= f;
+    store_e4m3<false>(static_cast<unsigned char*>(p.y) + o, 1, kNV, s);
+    if ((uint32_t)(gc + c) % (uint32_t)p.block == 0) p.scale[row * p.nb + (uint32_t)(gc + c) / (uint32_t)p.block] = sc;
   }
 }
 
@@ -268,7 +372,7 @@ __global__ void __launch_bounds__(256) wkv_norm_row(const NormParams p, bool x_b
       sum = fmaf(s, s, sum);
     }
     sum = cta_reduce<false>(sum, red);
-    if (threadIdx.x == 0) rstd[0] = 1.f / sqrtf(sum / (float)p.D + p.eps);
+    if (threadIdx.x == 0) rstd[0] = inv_root(fmaf(sum, p.inv_d, p.eps));
   } else {
     for (int g = w; g < p.G; g += nw) {  // a warp per group
       float sum = 0.f;
@@ -277,7 +381,7 @@ __global__ void __launch_bounds__(256) wkv_norm_row(const NormParams p, bool x_b
         sum = fmaf(s, s, sum);
       }
       sum = team_sum<32>(sum);
-      if (lane == 0) rstd[g] = 1.f / sqrtf(sum / (float)p.D + p.eps);
+      if (lane == 0) rstd[g] = inv_root(fmaf(sum, p.inv_d, p.eps));
     }
   }
   __threadfence_block();
@@ -299,7 +403,7 @@ __global__ void __launch_bounds__(256) wkv_norm_row(const NormParams p, bool x_b
   if (p.block == p.C) {
     float top = 0.f;
     for (int c = threadIdx.x; c < p.C; c += blockDim.x) top = fmaxf(top, fabsf(value(c)));
-    const float sc = e4m3_scale(cta_reduce<true>(top, red)), inv = 1.f / sc;
+    const float sc = e4m3_scale(cta_reduce<true>(top, red)), inv = rcp(sc);
     if (threadIdx.x == 0) p.scale[row] = sc;
     for (int c = threadIdx.x; c < p.C; c += blockDim.x) put(c, value(c), inv);
   } else {
@@ -311,7 +415,7 @@ __global__ void __launch_bounds__(256) wkv_norm_row(const NormParams p, bool x_b
         y[i] = i * 32 + lane < p.block ? value(b * p.block + i * 32 + lane) : 0.f;
         top = fmaxf(top, fabsf(y[i]));
       }
-      const float sc = e4m3_scale(lanes_max(top, 32)), inv = 1.f / sc;
+      const float sc = e4m3_scale(lanes_max(top, 32)), inv = rcp(sc);
       if (lane == 0) p.scale[row * nb + b] = sc;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -336,116 +440,147 @@ struct NormBwdParams {
   float* part;           // [nparts, C] sums of gy s r over each part's rows
   float* rstd;           // [N, G], wkv_norm_bwd_row only
   int nparts;
+  float inv_d;           // 1 / D
 };
 
 // Rows are dealt to CTAs (row = CTA, CTA + grid, ...). A CTA holds whole rows:
 // RPC rows at a time, each by its teams of TW lanes (one team per group) or by
-// all threads (TW = 0, one group), K vectors of 8 columns per thread. A thread
-// keeps the same columns from row to row and adds up its part of dweight in
-// registers; the RPC rows' parts are joined through shared memory at the end,
-// in a fixed order.
-template <typename Y, typename S, bool GS, int TW, int K>
-__global__ void __launch_bounds__(TW ? 512 : 1024) wkv_norm_bwd_team(const NormBwdParams p, int rpc) {
+// all threads (TW = 0, one group), K vectors of 8 columns per thread; SC as in
+// the forward. A thread keeps the same columns from row to row and adds up its
+// part of dweight in registers; the RPC rows' parts are joined through shared
+// memory at the end, in a fixed order. The next row is loaded while this one
+// is reduced (K <= 2: registers).
+template <typename Y, typename S, bool GS, int TW, int K, bool SC>
+__global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, int rpc) {
   extern __shared__ float acc[];  // [C], TW > 0 with rpc > 1
-  __shared__ float red[64];
+  __shared__ float2 red[2][16];
+  constexpr bool kAhead = K <= 2;  // also: the weights stay in registers
   const int tpr = TW ? TW * p.G : (int)blockDim.x;  // threads per row
   const int rl = TW ? (int)threadIdx.x / tpr : 0;   // row within the CTA's rpc rows
   const int tl = (int)threadIdx.x - rl * tpr;
-  const int g = TW ? tl / TW : 0;
+  const int gc = TW ? tl / TW * p.D : 0;            // the group's first column
   const int l = TW ? tl % (TW ? TW : 1) : tl;
   const int width = TW ? TW : tpr;
   const bool lane_on = rl < rpc;
   const long long step = (long long)gridDim.x * rpc;
-  float dw[K][kNV], w[K][kNV];
-  bool in[K];
+  float dw[K][kNV], wk[kAhead ? K : 1][kNV];
+  auto weights = [&](int k, float (&w)[kNV]) {
+    const Cols<SC> c(k, l, width, p.D);
+#pragma unroll
+    for (int e = 0; e < kNV; ++e) w[e] = 0.f;
+    if (lane_on && c.n > 0) {
+      Raw8<float, SC> wv;
+      wv.load(p.weight + gc + c.at, c.st, c.n);
+      wv.get(w);
+    }
+  };
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int col = (k * width + l) * kNV;
-    in[k] = lane_on && col < p.D;
 #pragma unroll
-    for (int e = 0; e < kNV; ++e) dw[k][e] = 0.f, w[k][e] = 0.f;
-    if (in[k]) {
-      Vec8<float> wv;
-      wv.load(p.weight + (long long)g * p.D + col);
-      wv.get(w[k]);
-    }
+    for (int e = 0; e < kNV; ++e) dw[k][e] = 0.f;
+    if (kAhead) weights(k, wk[kAhead ? k : 0]);
   }
-  for (long long row0 = (long long)blockIdx.x * rpc; row0 < p.N; row0 += step) {
+  Raw8<Y, SC> yv[K];
+  Raw8<S, SC> sv[K], gv[K];
+  auto load_ys = [&](long long row) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const Cols<SC> c(k, l, width, p.D);
+      if (lane_on && row < p.N && c.n > 0) {
+        yv[k].load(static_cast<const Y*>(p.gy) + row * p.C + gc + c.at, c.st, c.n);
+        sv[k].load(static_cast<const S*>(p.s) + row * p.s_st + gc + c.at, c.st, c.n);
+      }
+    }
+  };
+  auto load_g = [&](long long row) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const Cols<SC> c(k, l, width, p.D);
+      if (GS && lane_on && row < p.N && c.n > 0)
+        gv[k].load(static_cast<const S*>(p.gs) + row * p.C + gc + c.at, c.st, c.n);
+    }
+  };
+  long long row0 = (long long)blockIdx.x * rpc;
+  if (kAhead) load_ys(row0 + rl), load_g(row0 + rl);
+  for (int par = 0; row0 < p.N; row0 += step, par ^= 1) {
     const long long row = row0 + rl;
     const bool live = lane_on && row < p.N;
-    Vec8<Y> yv[K];
-    Vec8<S> sv[K], gv[K];
-    const long long o = row * p.C + (long long)g * p.D;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (live && in[k]) {
-        const int col = (k * width + l) * kNV;
-        yv[k].load(static_cast<const Y*>(p.gy) + o + col);
-        sv[k].load(static_cast<const S*>(p.s) + row * p.s_st + (long long)g * p.D + col);
-        if (GS) gv[k].load(static_cast<const S*>(p.gs) + o + col);
-      }
+    if (!kAhead) load_ys(row), load_g(row);
     float s[K][kNV], gy[K][kNV];
     float ss = 0.f, ps = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (live && in[k]) {
+      const Cols<SC> c(k, l, width, p.D);
+      if (live && c.n > 0) {
         yv[k].get(gy[k]);
         sv[k].get(s[k]);
       } else {
 #pragma unroll
         for (int e = 0; e < kNV; ++e) s[k][e] = gy[k][e] = 0.f;
       }
+      float(&w)[kNV] = wk[kAhead ? k : 0];
+      if (!kAhead) weights(k, w);
 #pragma unroll
       for (int e = 0; e < kNV; ++e) {
         ss = fmaf(s[k][e], s[k][e], ss);
-        ps = fmaf(gy[k][e] * w[k][e], s[k][e], ps);
+        ps = fmaf(gy[k][e] * w[e], s[k][e], ps);
       }
     }
+    if (kAhead) load_ys(row + step);
     if (TW) {
       ss = team_sum<TW ? TW : 32>(ss);
       ps = team_sum<TW ? TW : 32>(ps);
-    } else {  // both sums in one exchange
+    } else {  // both sums in one exchange; two buffers, one barrier per row
       const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, nw = blockDim.x >> 5;
       ss = team_sum<32>(ss);
       ps = team_sum<32>(ps);
+      if (lane == 0) red[par][wp] = make_float2(ss, ps);
       __syncthreads();
-      if (lane == 0) red[wp] = ss, red[32 + wp] = ps;
-      __syncthreads();
-      ss = team_sum<32>(lane < nw ? red[lane] : 0.f);
-      ps = team_sum<32>(lane < nw ? red[32 + lane] : 0.f);
+      const float2 v = lane < nw ? red[par][lane] : make_float2(0.f, 0.f);
+      ss = team_sum<32>(v.x);
+      ps = team_sum<32>(v.y);
     }
-    const float r = 1.f / sqrtf(ss / (float)p.D + p.eps);
-    const float m = ps / (float)p.D * r * r;
+    const float r = inv_root(fmaf(ss, p.inv_d, p.eps));
+    const float m = ps * p.inv_d * r * r;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (live && in[k]) {
+    for (int k = 0; k < K; ++k) {
+      const Cols<SC> c(k, l, width, p.D);
+      if (live && c.n > 0) {
         float d[kNV];
         if (GS) gv[k].get(d);
+        float(&w)[kNV] = wk[kAhead ? k : 0];
+        if (!kAhead) weights(k, w);
 #pragma unroll
         for (int e = 0; e < kNV; ++e) {
-          d[e] = (GS ? d[e] : 0.f) + r * (gy[k][e] * w[k][e] - s[k][e] * m);
+          const float t = gy[k][e] * w[e] - s[k][e] * m;
+          d[e] = GS ? fmaf(r, t, d[e]) : r * t;
           dw[k][e] = fmaf(gy[k][e], s[k][e] * r, dw[k][e]);
         }
-        Vec8<S>::store(static_cast<S*>(p.ds) + o + (k * width + l) * kNV, d);
+        Raw8<S, SC>::store(static_cast<S*>(p.ds) + row * p.C + gc + c.at, c.st, c.n, d);
       }
+    }
+    if (kAhead) load_g(row + step);
   }
   for (int turn = 0; turn < rpc; ++turn) {  // rows' parts join in order
     if (turn == rl && lane_on) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (in[k]) {
-          const int col = g * p.D + (k * width + l) * kNV;
-          if (turn > 0) {
+      for (int k = 0; k < K; ++k) {
+        const Cols<SC> c(k, l, width, p.D);
+        if (c.n <= 0) continue;
+        const int col = gc + c.at;
+        if (turn > 0) {
 #pragma unroll
-            for (int e = 0; e < kNV; ++e) dw[k][e] += acc[col + e];
-          }
-          if (turn == rpc - 1) {
-            Vec8<float>::store(p.part + (long long)blockIdx.x * p.C + col, dw[k]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < kNV; ++e) acc[col + e] = dw[k][e];
-          }
+          for (int e = 0; e < kNV; ++e)
+            if (!SC || e < c.n) dw[k][e] += acc[col + e * c.st];
         }
+        if (turn == rpc - 1) {
+          Raw8<float, SC>::store(p.part + (long long)blockIdx.x * p.C + col, c.st, c.n, dw[k]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kNV; ++e)
+            if (!SC || e < c.n) acc[col + e * c.st] = dw[k][e];
+        }
+      }
     }
     if (rpc > 1) __syncthreads();
   }
@@ -474,8 +609,8 @@ __global__ void __launch_bounds__(256) wkv_norm_bwd_row(const NormBwdParams p, b
       ss = team_sum<32>(ss);
       ps = team_sum<32>(ps);
     }
-    const float r = 1.f / sqrtf(ss / (float)p.D + p.eps);
-    const float m = ps / (float)p.D * r * r;
+    const float r = inv_root(fmaf(ss, p.inv_d, p.eps));
+    const float m = ps * p.inv_d * r * r;
     if (at == 0) p.rstd[row * p.G + g] = r;
     for (int i = at; i < p.D; i += step) {
       const int c = g * p.D + i;
@@ -498,21 +633,21 @@ __global__ void __launch_bounds__(256) wkv_norm_bwd_cols(const NormBwdParams p, 
   p.part[(long long)blockIdx.y * p.C + c] = dw;
 }
 
-// dweight = the parts' sum, in a fixed order: 8 warps add every eighth part of
-// 32 columns, then join.
-__global__ void __launch_bounds__(256) wkv_norm_bwd_join(const float* part, int nparts, int C, float* dw) {
-  __shared__ float sm[8][32];
+// dweight = the parts' sum, in a fixed order: of 32 columns, each of 32 warps
+// adds every 32nd part, then a warp joins the 32 sums of a column.
+__global__ void __launch_bounds__(1024) wkv_norm_bwd_join(const float* part, int nparts, int C, float* dw) {
+  __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  if (c < C)
-    for (int i = w; i < nparts; i += 8) a += part[(long long)i * C + c];
+  if (c < C) {
+#pragma unroll 8
+    for (int i = w; i < nparts; i += 32) a += part[(long long)i * C + c];
+  }
   sm[w][lane] = a;
   __syncthreads();
-  if (w == 0 && c < C) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) a += sm[i][lane];
-    dw[c] = a;
-  }
+  // warp w joins column w's 32 sums, lane by lane
+  a = team_sum<32>(sm[lane][w]);
+  if (lane == 0 && blockIdx.x * 32 + w < C) dw[blockIdx.x * 32 + w] = a;
 }
 
 }  // namespace wkv
