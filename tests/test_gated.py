@@ -18,6 +18,7 @@ P = ctypes.c_void_p
 @pytest.fixture(scope="module")
 def L():
     wbuild.build()
+    wbuild.build_ext()
     return _abi.lib()
 
 
@@ -74,7 +75,7 @@ def test_refusals_before_any_launch(L):
         E.WKV_ERR_INVALID_ARG
 
 
-def test_binding_refuses_cpu_tensors_and_names_the_argument():
+def test_binding_refuses_cpu_tensors_and_names_the_argument(L):
     x = torch.zeros(1, 2, 3)
     for call in (lambda: W.gated_forward(x, x), lambda: W.gated_backward(x, x, x),
                  lambda: W.gated_step(x[0], x[0], x[0]), lambda: W.Gated.apply(x, x)):

@@ -18,6 +18,7 @@ P = ctypes.c_void_p
 @pytest.fixture(scope="module")
 def L():
     wbuild.build()
+    wbuild.build_ext()
     return _abi.lib()
 
 
@@ -62,7 +63,7 @@ def test_refusals_before_any_launch(L):
     assert L.wkv_rms_norm_backward_workspace_size(4, 0, 1) == 256 == L.wkv_rms_norm_backward_workspace_size(0, 0, 1)
 
 
-def test_binding_refuses_cpu_tensors_and_names_the_argument():
+def test_binding_refuses_cpu_tensors_and_names_the_argument(L):
     x, w = torch.zeros(2, 8), torch.ones(8)
     for call, name in ((lambda: W.rms_norm(x, w), "x"), (lambda: W.rms_norm_quant(x, w), "x"),
                        (lambda: W.rms_norm_backward(x, x, w), "s"), (lambda: W.RMSNorm.apply(x, w), "x")):

@@ -1,4 +1,4 @@
-"""Build libwkv.so in-tree with nvcc for sm_100a (Blackwell B200).
+"""Build libwkv.so in-tree with nvcc for sm_100a (Blackwell B200), and _wkv_torch.so with g++.
 
     python -m wkv_recurrence_b200.build            # build if sources changed
     python -m wkv_recurrence_b200.build --force    # always rebuild
@@ -24,7 +24,9 @@ MAIN = os.path.join(SRC_DIR, "wkv_api.cu")
 GATED = os.path.join(SRC_DIR, "wkv_gated.cu")
 NORM = os.path.join(SRC_DIR, "wkv_norm.cu")
 HOST = os.path.join(SRC_DIR, "wkv_host.cpp")  # host-side streaming of host-resident sequences
+TORCH = os.path.join(SRC_DIR, "wkv_torch.cpp")  # the Python calling path of the newer entry points
 LIB = os.path.join(HERE, "_build", "libwkv.so")
+EXT = os.path.join(HERE, "_build", "_wkv_torch.so")
 LIB_DEBUG = os.path.join(HERE, "_build", "libwkv_debug.so")
 HEADER = os.path.join(ROOT, "include", "wkv.h")
 
@@ -37,9 +39,8 @@ NVCC_FLAGS = [
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(SRC_DIR, "*.cu")) + glob.glob(os.path.join(SRC_DIR, "*.cuh"))
-                  + glob.glob(os.path.join(SRC_DIR, "*.cpp")) + glob.glob(os.path.join(SRC_DIR, "*.h"))
-                  + [HEADER])
+    found = [p for pat in ("*.cu", "*.cuh", "*.cpp", "*.h") for p in glob.glob(os.path.join(SRC_DIR, pat))]
+    return sorted(p for p in found if p != TORCH) + [HEADER]
 
 
 def nvcc() -> str:
@@ -64,11 +65,35 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     return out
 
 
+def build_ext(force: bool = False, verbose: bool = False) -> str:
+    """_wkv_torch.so: host code against the installed torch's headers."""
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(p) for p in (TORCH, HEADER)):
+        return EXT
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.sep in nvcc() else "/usr/local/cuda"
+    os.makedirs(os.path.dirname(EXT), exist_ok=True)
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-I{base}/include", f"-I{base}/include/torch/csrc/api/include", f"-I{cuda}/include",
+           f"-I{sysconfig.get_paths()['include']}", "-o", tmp, TORCH,
+           f"-L{base}/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build_all(force: bool = False, verbose: bool = False):
-    """Both variants, compiled concurrently."""
+    """Both variants and the Python calling path, compiled concurrently."""
     from concurrent.futures import ThreadPoolExecutor
-    with ThreadPoolExecutor(2) as ex:
+    with ThreadPoolExecutor(3) as ex:
         futs = [ex.submit(build, force, verbose, (), d) for d in (False, True)]
+        futs.append(ex.submit(build_ext, force, verbose))
         return [f.result() for f in futs]
 
 
@@ -77,3 +102,4 @@ if __name__ == "__main__":
         print(build_all(force="--force" in sys.argv, verbose=True))
     else:
         print(build(force="--force" in sys.argv, verbose=True))
+        print(build_ext(force="--force" in sys.argv, verbose=True))
