@@ -168,6 +168,12 @@ wkv_status pass_state(const float* in, float* out, int64_t n, cudaStream_t st) {
   return cuda_ok(e) ? WKV_OK : WKV_ERR_CUDA;
 }
 
+Divisor divisor(uint32_t d) {
+  int s = 0;
+  while ((1ull << s) < d) ++s;
+  return Divisor{d, (uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 void chain(GatedParams* p, const GatedPlan& pl, void* workspace) {
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p->NG = pl.NG;
@@ -175,6 +181,8 @@ void chain(GatedParams* p, const GatedPlan& pl, void* workspace) {
   p->G = pl.G;
   p->ngrp = pl.ngrp;
   p->tiles = pl.tiles;
+  p->by_items = divisor((uint32_t)p->B * (uint32_t)pl.NG);
+  p->by_ng = divisor((uint32_t)pl.NG);
   p->hdr = reinterpret_cast<WsHeader*>(ws);
   p->tot = reinterpret_cast<GatedRec*>(ws + pl.off_tot);
   p->pre = reinterpret_cast<GatedRec*>(ws + pl.off_pre);

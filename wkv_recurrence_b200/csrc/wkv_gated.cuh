@@ -271,6 +271,15 @@ __device__ __forceinline__ bool rec_load(const GatedRec* r, uint64_t tag, float&
 
 constexpr uint64_t kGatedTag = 0x47415445ull << 32;  // tag = kGatedTag + the launch's number on this workspace
 
+// t / d for t < 2^31 as a product: m = ceil(2^sh / d) with sh = 31 + ceil(log2
+// d) exceeds 2^sh / d by less than one, which t / 2^31 < 1 of a unit in the
+// quotient's 2^-ceil(log2 d) cannot reach.
+struct Divisor {
+  uint32_t d, m;
+  int sh;
+  __device__ __forceinline__ uint32_t of(uint32_t t) const { return (uint32_t)(((uint64_t)t * m) >> sh); }
+};
+
 struct GatedParams {
   int B, T, C;
   int NG;      // channel groups of 64 per batch row
@@ -278,6 +287,7 @@ struct GatedParams {
   int G;       // tiles per look-back group
   int ngrp;    // look-back groups per sequence
   long long tiles;
+  Divisor by_items, by_ng;  // B NG and NG
   const void* x;
   const void* z;
   long long x_sb, x_st, z_sb, z_st;  // element strides of the batch and token axes
@@ -444,16 +454,20 @@ __device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, in
 // The tiles of a CTA. Several tiles per sequence: by tickets, so that every
 // tile's predecessors have been taken before it. One: dealt out.
 struct Tile {
-  int pos, item, b, c0;  // position along the scan, channel group, batch row, first channel of the lane
+  int pos, item, b, cg;  // position along the scan (-1: no more tiles), channel group, batch row, first channel
 };
 __device__ __forceinline__ Tile gated_tile(const GatedParams& p, long long t) {
-  const int items = p.B * p.NG;
+  if (t >= p.tiles) return Tile{-1, 0, 0, 0};
   Tile r;
-  r.pos = (int)((uint32_t)t / (uint32_t)items);
-  r.item = (int)((uint32_t)t % (uint32_t)items);
-  r.b = r.item / p.NG;
-  r.c0 = (r.item % p.NG) * kGatedCG + (threadIdx.x & 31) * 2;
+  r.pos = (int)p.by_items.of((uint32_t)t);
+  r.item = (int)((uint32_t)t - (uint32_t)r.pos * p.by_items.d);
+  r.b = (int)p.by_ng.of((uint32_t)r.item);
+  r.cg = (r.item - r.b * p.NG) * kGatedCG;
   return r;
+}
+// The ticket after `last` (thread 0).
+__device__ __forceinline__ long long gated_ticket(const GatedParams& p, long long last) {
+  return p.nch > 1 ? (long long)atomicAdd(&p.hdr->ticket, 1u) : last + gridDim.x;
 }
 
 // Thread 0 counts the CTA out; the last one readies the header for the next
@@ -475,7 +489,7 @@ struct GatedShared {
   Span agg[2][NWMAX][32];   // the warps' spans, by parity of the tile
   float2 rev[2][NWMAX][32];  // backward: their gradients (the P is the same)
   Front<NWMAX> front;
-  long long next[2];
+  long long next[2];        // by parity: the ticket after this one
   uint32_t epoch;
 };
 
@@ -498,41 +512,38 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
   X* sx = reinterpret_cast<X*>(tiles) + (size_t)w * J * kGatedCG;
   Z* sz = reinterpret_cast<Z*>(tiles + (size_t)NW * J * kGatedCG * sizeof(X)) + (size_t)w * J * kGatedCG;
 
-  auto fetch = [&](long long t, const Tile& a) {  // this warp's inputs of tile t, on their way to shared memory
-    if (t < p.tiles) {
-      const int t0 = a.pos * L + w * J, c0 = a.c0 - lane * 2;
-      const int rows = min(J, p.T - t0), left = p.C - c0;
-      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, static_cast<const X*>(p.x), p.x_st,
-                      rows, left, p.x_gran);
-      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, static_cast<const Z*>(p.z), p.z_st,
-                      rows, left, p.z_gran);
+  auto fetch = [&](const Tile& a) {  // this warp's inputs of a tile, on their way to shared memory
+    if (a.pos >= 0) {
+      const int t0 = a.pos * L + w * J;
+      const int rows = min(J, p.T - t0), left = p.C - a.cg;
+      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + a.cg, static_cast<const X*>(p.x),
+                      p.x_st, rows, left, p.x_gran);
+      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + a.cg, static_cast<const Z*>(p.z),
+                      p.z_st, rows, left, p.z_gran);
     }
     copy_commit();
   };
 
-  long long cur = blockIdx.x;
-  uint64_t tag = 0;
-  if (chained) {
-    if (threadIdx.x == 0) {
-      sh.next[0] = atomicAdd(&p.hdr->ticket, 1u);
-      sh.epoch = *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch);
-    }
-    __syncthreads();
-    cur = sh.next[0];
-    tag = kGatedTag + sh.epoch + 1u;
+  long long ticket = (long long)blockIdx.x - gridDim.x;  // thread 0's last one
+  if (threadIdx.x == 0) {
+    ticket = gated_ticket(p, ticket);
+    sh.next[0] = ticket;
+    sh.epoch = chained ? *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch) : 0;
   }
-  Tile a = gated_tile(p, cur);
-  fetch(cur, a);
-  for (int par = 0; cur < p.tiles; par ^= 1) {
+  __syncthreads();
+  Tile a = gated_tile(p, sh.next[0]);
+  const uint64_t tag = kGatedTag + sh.epoch + 1u;
+  fetch(a);
+  for (int par = 1; a.pos >= 0; par ^= 1) {
     const int t0 = a.pos * L + w * J;
     const int nt = p.T - t0;  // tokens from this span on
-    long long ticket = cur + gridDim.x;
-    if (chained && threadIdx.x == 0) ticket = atomicAdd(&p.hdr->ticket, 1u);
+    const int c0 = a.cg + lane * 2;
+    if (threadIdx.x == 0) ticket = gated_ticket(p, ticket);
     // The state before the sequence enters the scan at its first tile alone:
     // its total, which carries it on, depends on this load, so h_out may be
     // h0. (In a single tile the barrier below stands between this load and
     // that store.)
-    const float2 first = p.h0 && a.pos == 0 ? row_get(p.h0, (long long)a.b * p.C, a.c0, p.C) : splat(0.f);
+    const float2 first = p.h0 && a.pos == 0 ? row_get(p.h0, (long long)a.b * p.C, c0, p.C) : splat(0.f);
     const Head ask = head_ask(p, a.item, a.pos, tag, first);
 
     copy_wait();
@@ -557,9 +568,8 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     if (threadIdx.x == 0) sh.next[par] = ticket;
     __syncthreads();
     forget(coef);
-    const long long nxt = sh.next[par];
-    const Tile an = gated_tile(p, nxt);
-    fetch(nxt, an);  // every lane's reads of the tile lie before the barrier
+    const Tile an = gated_tile(p, sh.next[par]);
+    fetch(an);  // every lane's reads of the tile lie before the barrier
 
     float2 h;  // the state in front of the tile
     if (chained && p.G > 1) {
@@ -576,14 +586,14 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
       h = head_get(p, a.item, a.pos, tag, ask);
     }
     if (p.marks && w == 0)
-      row_put(p.hdr, p.marks, ((long long)a.b * p.nch + a.pos) * p.C, a.c0, p.C, (size_t)p.B * p.nch * p.C, h);
+      row_put(p.hdr, p.marks, ((long long)a.b * p.nch + a.pos) * p.C, c0, p.C, (size_t)p.B * p.nch * p.C, h);
     for (int i = 0; i < w; ++i) h = apply(sh.agg[par][i][lane], h);
     if (chained && p.G == 1 && w == NW - 1 && a.pos != p.nch - 1)  // the state after this tile
       rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos) * kGatedCG + lane * 2,
               (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), apply(s, h), tag);
     // replay
-    O* op = static_cast<O*>(p.out) + ((long long)a.b * p.T + t0) * p.C + a.c0;
-    const bool store = p.out && a.c0 < p.C;
+    O* op = static_cast<O*>(p.out) + ((long long)a.b * p.T + t0) * p.C + c0;
+    const bool store = p.out && c0 < p.C;
     if (nt >= J && p.pair) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -596,13 +606,12 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
       for (int j = 0; j < J; ++j) {
         h = gate_step(gate_base(coef[j]), coef[j], h, in[j]);
         if (store && j < nt && WKV_IN(p.hdr, op - static_cast<O*>(p.out), (size_t)p.B * p.T * p.C))
-          store_one(op, h, a.c0 + 1 < p.C);
+          store_one(op, h, c0 + 1 < p.C);
         op += p.C;
       }
     }
     if (p.h_out && nt > 0 && nt <= J)  // this span holds the last token
-      row_put(p.hdr, p.h_out, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, h);
-    cur = nxt;
+      row_put(p.hdr, p.h_out, (long long)a.b * p.C, c0, p.C, (size_t)p.B * p.C, h);
     a = an;
   }
   if (chained) gated_leave(p, sh.epoch);
@@ -637,56 +646,54 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
   Z* sz = reinterpret_cast<Z*>(tiles + row * sizeof(X)) + mine;
   O* sg0 = reinterpret_cast<O*>(tiles + row * (sizeof(X) + sizeof(Z))) + mine;
 
-  auto fetch_xz = [&](long long t, const Tile& a) {
-    if (t < p.tiles) {
-      const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
-      const int rows = min(J, p.T - t0), left = p.C - c0;
-      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + c0, static_cast<const X*>(p.x), p.x_st,
-                      rows, left, p.x_gran);
-      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + c0, static_cast<const Z*>(p.z), p.z_st,
-                      rows, left, p.z_gran);
+  auto fetch_xz = [&](const Tile& a) {
+    if (a.pos >= 0) {
+      const int t0 = (p.nch - 1 - a.pos) * L + w * J;
+      const int rows = min(J, p.T - t0), left = p.C - a.cg;
+      copy_span<X, J>(sx, static_cast<const X*>(p.x) + a.b * p.x_sb + t0 * p.x_st + a.cg, static_cast<const X*>(p.x),
+                      p.x_st, rows, left, p.x_gran);
+      copy_span<Z, J>(sz, static_cast<const Z*>(p.z) + a.b * p.z_sb + t0 * p.z_st + a.cg, static_cast<const Z*>(p.z),
+                      p.z_st, rows, left, p.z_gran);
     }
   };
-  auto fetch_g = [&](long long t, const Tile& a, O* dst) {
-    if (t < p.tiles) {
-      const int t0 = (p.nch - 1 - a.pos) * L + w * J, c0 = a.c0 - lane * 2;
-      copy_span<O, J>(dst, static_cast<const O*>(p.g) + ((long long)a.b * p.T + t0) * p.C + c0, static_cast<const O*>(p.g),
-                      p.C, min(J, p.T - t0), p.C - c0, p.g_gran);
+  auto fetch_g = [&](const Tile& a, O* dst) {
+    if (a.pos >= 0) {
+      const int t0 = (p.nch - 1 - a.pos) * L + w * J;
+      copy_span<O, J>(dst, static_cast<const O*>(p.g) + ((long long)a.b * p.T + t0) * p.C + a.cg,
+                      static_cast<const O*>(p.g), p.C, min(J, p.T - t0), p.C - a.cg, p.g_gran);
     }
   };
 
-  long long cur = blockIdx.x;
-  uint64_t tag = 0;
-  if (chained) {
-    if (threadIdx.x == 0) {
-      sh.next[0] = atomicAdd(&p.hdr->ticket, 1u);
-      sh.epoch = *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch);
-    }
-    __syncthreads();
-    cur = sh.next[0];
-    tag = kGatedTag + sh.epoch + 1u;
+  long long ticket = (long long)blockIdx.x - gridDim.x;  // thread 0's last one
+  if (threadIdx.x == 0) {
+    ticket = gated_ticket(p, ticket);
+    sh.next[0] = ticket;
+    sh.epoch = chained ? *reinterpret_cast<volatile uint32_t*>(&p.hdr->epoch) : 0;
   }
-  Tile a = gated_tile(p, cur);
-  fetch_xz(cur, a);
-  fetch_g(cur, a, sg0);
+  __syncthreads();
+  Tile a = gated_tile(p, sh.next[0]);
+  const uint64_t tag = kGatedTag + sh.epoch + 1u;
+  fetch_xz(a);
+  fetch_g(a, sg0 + (kGB == 2 ? row : 0));
   copy_commit();
-  for (int par = 0; cur < p.tiles; par ^= 1) {
+  for (int par = 1; a.pos >= 0; par ^= 1) {
     const int chunk = p.nch - 1 - a.pos;  // position in the sequence
     const int t0 = chunk * L + w * J;
     const int nt = p.T - t0;
+    const int c0 = a.cg + lane * 2;
     O* sg = sg0 + (kGB == 2 && par ? row : 0);
-    long long ticket = cur + gridDim.x;
-    if (chained && threadIdx.x == 0) ticket = atomicAdd(&p.hdr->ticket, 1u);
+    if (threadIdx.x == 0) ticket = gated_ticket(p, ticket);
     // gradient behind the sequence (it enters at the scan's first tile alone,
     // as in the forward), state in front of the tile
-    const float2 first = p.dh_out && a.pos == 0 ? row_get(p.dh_out, (long long)a.b * p.C, a.c0, p.C) : splat(0.f);
-    float2 h = chained ? row_get(p.marks, ((long long)a.b * p.nch + chunk) * p.C, a.c0, p.C)
-                       : (p.h0 ? row_get(p.h0, (long long)a.b * p.C, a.c0, p.C) : splat(0.f));
+    const float2 first = p.dh_out && a.pos == 0 ? row_get(p.dh_out, (long long)a.b * p.C, c0, p.C) : splat(0.f);
+    float2 h = chained ? row_get(p.marks, ((long long)a.b * p.nch + chunk) * p.C, c0, p.C)
+                       : (p.h0 ? row_get(p.h0, (long long)a.b * p.C, c0, p.C) : splat(0.f));
     const Head ask = head_ask(p, a.item, a.pos, tag, first);
 
     copy_wait();
     __syncwarp();
     Span s{splat(1.f), splat(0.f)};
+    float2 Q = splat(0.f);  // the span's gradient in front of it, from none behind: the sum of P_t g_t, P_t = f_1 .. f_t
     float2 coef[J], e[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -696,20 +703,15 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
       const float2 A = gate_base(coef[j]);
       s.H = gate_step(A, coef[j], s.H, in);
       s.P = gate_mul(A, coef[j], s.P);
+      Q = fma2(s.P, load2(sg + j * kGatedCG + lane * 2), Q);
       if (j % 4 == 3) asm volatile("" ::: "memory");  // four tokens' loads and exponentials at a time: registers
     }
-    forget(coef);
-    float2 Q = splat(0.f);
-#pragma unroll
-    for (int j = J - 1; j >= 0; --j)
-      Q = gate_mul(gate_base(coef[j]), coef[j], add2(load2(sg + j * kGatedCG + lane * 2), Q));
     sh.agg[par][w][lane] = s;
     sh.rev[par][w][lane] = Q;
     if (threadIdx.x == 0) sh.next[par] = ticket;
     __syncthreads();
     forget(coef);
-    const long long nxt = sh.next[par];
-    const Tile an = gated_tile(p, nxt);
+    const Tile an = gated_tile(p, sh.next[par]);
     // the states of this span, and with them what D is multiplied by in dz
     for (int i = 0; i < w; ++i) h = apply(sh.agg[par][i][lane], h);
 #pragma unroll
@@ -721,8 +723,8 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     }
     forget(coef);
     __syncwarp();
-    fetch_xz(nxt, an);
-    if (kGB == 2) fetch_g(nxt, an, sg0 + (par ? 0 : row));
+    fetch_xz(an);
+    if (kGB == 2) fetch_g(an, sg0 + (par ? 0 : row));
     copy_commit();
     float2 q;  // f_{t+1} D_{t+1}, what flows back into token t
     if (chained && p.G > 1) {
@@ -742,8 +744,8 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     if (chained && p.G == 1 && w == 0 && a.pos != p.nch - 1)
       rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos) * kGatedCG + lane * 2,
               (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), fma2(s.P, q, Q), tag);
-    long long o = ((long long)a.b * p.T + t0 + J - 1) * p.C + a.c0;
-    const bool on = a.c0 < p.C;
+    long long o = ((long long)a.b * p.T + t0 + J - 1) * p.C + c0;
+    const bool on = c0 < p.C;
     if (nt >= J && p.pair) {
 #pragma unroll
       for (int j = J - 1; j >= 0; --j) {
@@ -761,19 +763,18 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
         const float2 A = gate_base(coef[j]), D = add2(load2(sg + j * kGatedCG + lane * 2), q);
         q = gate_mul(A, coef[j], D);
         if (on && j < nt && WKV_IN(p.hdr, o, (size_t)p.B * p.T * p.C)) {
-          store_one(static_cast<X*>(p.dx) + o, Gt::input(A, coef[j], D), a.c0 + 1 < p.C);
-          store_one(static_cast<Z*>(p.dz) + o, mul2(D, e[j]), a.c0 + 1 < p.C);
+          store_one(static_cast<X*>(p.dx) + o, Gt::input(A, coef[j], D), c0 + 1 < p.C);
+          store_one(static_cast<Z*>(p.dz) + o, mul2(D, e[j]), c0 + 1 < p.C);
         }
         o -= p.C;
       }
     }
-    if (p.dh0 && chunk == 0 && w == 0) row_put(p.hdr, p.dh0, (long long)a.b * p.C, a.c0, p.C, (size_t)p.B * p.C, q);
+    if (p.dh0 && chunk == 0 && w == 0) row_put(p.hdr, p.dh0, (long long)a.b * p.C, c0, p.C, (size_t)p.B * p.C, q);
     if (kGB == 1) {
       __syncwarp();
-      fetch_g(nxt, an, sg0);
+      fetch_g(an, sg0);
       copy_commit();
     }
-    cur = nxt;
     a = an;
   }
   if (chained) gated_leave(p, sh.epoch);
