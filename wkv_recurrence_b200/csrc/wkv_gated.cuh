@@ -21,9 +21,9 @@
 //          its own (one record) and the totals of the tiles before it in its
 //          group, so the sequence is walked in T/(L G) hops and every sum has
 //          one fixed order.
-//   replay with the state in front of its span, each warp runs its tokens
-//          again from registers and stores. Inputs are read once, outputs
-//          written once.
+//   output with the state in front of its span, each warp has its tokens'
+//          states from what the fold kept in registers (the backward runs its
+//          tokens again). Inputs are read once, outputs written once.
 // A record is 16 bytes, {P, H, tag}, moved by one 128-bit access, so its tag
 // (the launch's number) vouches for its data without a fence, and a reader
 // polls the data itself.
@@ -548,26 +548,21 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
 
     copy_wait();
     __syncwarp();
+    // fold, keeping for every token the span up to it: h_t = P_t h + H_t. A
+    // token past the end (its x is 0) changes nothing: f = 1.
     Span s{splat(1.f), splat(0.f)};
-    float2 coef[J], in[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      coef[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2), load2(sx + j * kGatedCG + lane * 2), in[j]);
-    if (nt < J) {  // tokens past the end (their x is 0) change nothing: f = 1
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (j >= nt) coef[j] = splat(kGateHeld);
-    }
+    float2 P[J], H[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const float2 A = gate_base(coef[j]);
-      s.H = gate_step(A, coef[j], s.H, in[j]);
-      s.P = gate_mul(A, coef[j], s.P);
+      P[j] = Gt::coef(load2(sz + j * kGatedCG + lane * 2), load2(sx + j * kGatedCG + lane * 2), H[j]);
+      if (nt < J && j >= nt) P[j] = splat(kGateHeld);
+      const float2 A = gate_base(P[j]);
+      s.H = H[j] = gate_step(A, P[j], s.H, H[j]);
+      s.P = P[j] = gate_mul(A, P[j], s.P);
     }
     sh.agg[par][w][lane] = s;
     if (threadIdx.x == 0) sh.next[par] = ticket;
     __syncthreads();
-    forget(coef);
     const Tile an = gated_tile(p, sh.next[par]);
     fetch(an);  // every lane's reads of the tile lie before the barrier
 
@@ -591,25 +586,24 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     if (chained && p.G == 1 && w == NW - 1 && a.pos != p.nch - 1)  // the state after this tile
       rec_put(p, p.pre, ((size_t)a.item * p.ngrp + a.pos) * kGatedCG + lane * 2,
               (size_t)p.B * p.NG * p.ngrp * kGatedCG, splat(0.f), apply(s, h), tag);
-    // replay
     O* op = static_cast<O*>(p.out) + ((long long)a.b * p.T + t0) * p.C + c0;
     const bool store = p.out && c0 < p.C;
     if (nt >= J && p.pair) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        h = gate_step(gate_base(coef[j]), coef[j], h, in[j]);
-        if (store && WKV_IN(p.hdr, op + 1 - static_cast<O*>(p.out), (size_t)p.B * p.T * p.C)) store2(op, h);
+        if (store && WKV_IN(p.hdr, op + 1 - static_cast<O*>(p.out), (size_t)p.B * p.T * p.C))
+          store2(op, fma2(P[j], h, H[j]));
         op += p.C;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        h = gate_step(gate_base(coef[j]), coef[j], h, in[j]);
         if (store && j < nt && WKV_IN(p.hdr, op - static_cast<O*>(p.out), (size_t)p.B * p.T * p.C))
-          store_one(op, h, c0 + 1 < p.C);
+          store_one(op, fma2(P[j], h, H[j]), c0 + 1 < p.C);
         op += p.C;
       }
     }
+    h = apply(s, h);
     if (p.h_out && nt > 0 && nt <= J)  // this span holds the last token
       row_put(p.hdr, p.h_out, (long long)a.b * p.C, c0, p.C, (size_t)p.B * p.C, h);
     a = an;
