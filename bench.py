@@ -186,11 +186,14 @@ def measured_peaks():
 
 
 def source_digest() -> str:
-    """Hash of the kernels and of the code that chooses and launches them (tile
-    shapes, stages and grids change the traffic a capture records)."""
+    """Hash of the WKV kernels and of the code that chooses and launches them
+    (tile shapes, stages and grids change the traffic a capture records). The
+    gated recurrence and the norm are separate translation units."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "wkv_recurrence_b200", "csrc")
     for p in sorted(glob.glob(os.path.join(csrc, "*.cuh")) + glob.glob(os.path.join(csrc, "*.cu"))):
+        if os.path.basename(p).startswith(("wkv_gated.", "wkv_norm.")):
+            continue
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())
             h.update(f.read())
@@ -730,6 +733,102 @@ def measure_v6(wl, args, device):
     return rec
 
 
+# Sub-records of the gated recurrence and the RMS norm, by --part alone: the
+# layer, long and decode shapes of the WKV workloads, and the norm at a
+# prefill's size.
+OPERATOR_PARTS = ("gated_layer", "gated_long", "gated_decode", "norm", "norm_quant", "norm_backward")
+
+
+def measure_operator(part, args, device):
+    """One of OPERATOR_PARTS: per-call time in a CUDA graph over rotating buffer
+    sets, against the bytes that the call cannot do without (each input read
+    and each output written once). gated_layer and gated_long are training
+    steps: the forward and its backward."""
+    import torch
+
+    import wkv_recurrence_b200 as W
+
+    gen = torch.Generator(device=device).manual_seed(1)
+    f32, bf16 = torch.float32, torch.bfloat16
+
+    def normal(shape, dtype=f32, scale=1.0):
+        return (torch.randn(shape, generator=gen, device=device) * scale).to(dtype)
+
+    if part.startswith("gated"):
+        B, T, C, dt = {"gated_layer": (8, 1024, 768, bf16), "gated_long": (1, 65536, 2048, f32),
+                       "gated_decode": (4096, 1, 768, bf16)}[part]
+        n, es = B * T * C, 2 if dt == bf16 else 4
+
+        def make():
+            x, z = normal((B, T, C), dt), (normal((B, T, C), scale=1.5) + 4.0).to(dt)
+            d = dict(x=x, z=z, h=normal((B, C)), out=torch.empty_like(x), s=torch.empty(B, C, device=device))
+            if part != "gated_decode":
+                d.update(g=normal((B, T, C), dt), marks=W.gated_checkpoints(x),
+                         ws=torch.zeros(W.gated_workspace_size(B, T, C), dtype=torch.uint8, device=device))
+            return d
+
+        def call(d, h=None):
+            if part == "gated_decode":
+                W.gated_step(d["h"], d["x"][:, 0], d["z"][:, 0], out=d["out"][:, 0], state_out=d["s"])
+            else:
+                W.gated_forward(d["x"], d["z"], d["h"], out=d["out"], state_out=d["s"], checkpoints=d["marks"],
+                                workspace=d["ws"])
+                W.gated_backward(d["x"], d["z"], d["g"], d["h"], checkpoints=d["marks"], workspace=d["ws"])
+
+        algo = n * 3 * es + 8 * n if part == "gated_decode" else n * 8 * es
+        what = "gated_step" if part == "gated_decode" else "gated_forward + gated_backward"
+        desc, launches = f"{what} {B} x {T} x {C} {'bf16' if dt == bf16 else 'fp32'}", 1 if part == "gated_decode" else 2
+    else:
+        N, C = (65536, 2048) if part == "norm_backward" else (65536, 4096)
+        n = N * C
+        w = 1 + normal((C,), scale=0.2)
+
+        def make():
+            d = dict(x=normal((N, C), bf16), r=normal((N, C), bf16, 3.0))
+            if part == "norm_backward":
+                d["gs"] = normal((N, C), bf16)
+            return d
+
+        def call(d, h=None):
+            if part == "norm":
+                W.rms_norm(d["x"], w, d["r"])
+            elif part == "norm_quant":
+                W.rms_norm_quant(d["x"], w, d["r"], block=128)
+            else:
+                W.rms_norm_backward(d["x"], d["r"], w, d["gs"])
+
+        algo = n * {"norm": 8, "norm_quant": 7, "norm_backward": 8}[part]
+        what = {"norm": "rms_norm", "norm_quant": "rms_norm_quant", "norm_backward": "rms_norm_backward"}[part]
+        desc, launches = f"{what} {N} x {C} bf16, residual", 2 if part == "norm_backward" else 1
+    l2 = torch.cuda.get_device_properties(device).L2_cache_size
+    R = int(min(6, max(2, -(-int(2.5 * l2) // algo))))
+    sets = [make() for _ in range(R)]
+    stream = torch.cuda.current_stream(device)
+    for i in range(max(3, args.warmup)):
+        call(sets[i % R])
+    torch.cuda.synchronize(device)
+    graph = _capture(sets, call, stream, device)
+    graph.replay()
+    torch.cuda.synchronize(device)
+    n_rep = max(1, -(-max(1, args.steps // 20) // R))
+    sampler = ClockSampler(torch.cuda.current_device()) if not args.no_clocks else None
+    if sampler:
+        sampler.start()
+    ms = _timed_graph(graph, n_rep, stream, device)
+    clocks = sampler.stop() if sampler else None
+    call_ms = ms / (n_rep * R)
+    peak, peak_kind = measured_peaks()
+    achieved = algo / (call_ms / 1e3) / 1e9
+    rec = {"workload": desc, "name": part, "value": n / (call_ms / 1e3), "unit": "elements/s", "steps": n_rep * R,
+           "ms_per_step": call_ms,
+           "roofline": {"bound": "hbm", "kernel": what, "achieved": achieved, "peak": peak, "peak_source": peak_kind,
+                        "unit": "GB/s", "frac": achieved / peak, "algorithmic_bytes": algo, "launch_ms": call_ms},
+           "gpu_launches": launches * n_rep * R, "clocks": clocks, "buffer_sets": R}
+    del graph, sets
+    torch.cuda.empty_cache()
+    return rec
+
+
 def run_ours(args):
     import torch
 
@@ -744,6 +843,8 @@ def run_ours(args):
         from wkv_recurrence_b200 import inputs as I
         if args.part.startswith("backward_"):
             rec = measure_backward(workload(args, args.part[len("backward_"):], override=True), args, device)
+        elif args.part in OPERATOR_PARTS:
+            rec = measure_operator(args.part, args, device)
         else:
             rec = measure_v6(I.V6_WORKLOADS[args.part], args, device)
         if rank == 0:
@@ -1019,7 +1120,7 @@ def main(argv=None):
     ap.add_argument("--no-e2e", action="store_true")
     ap.add_argument("--no-cpu", action="store_true")
     ap.add_argument("--no-sub", action="store_true", help="headline workload only (no per-workload sub-records)")
-    ap.add_argument("--part", choices=["backward_layer", "backward_long", "v6", "v6_bf16"], default="",
+    ap.add_argument("--part", choices=["backward_layer", "backward_long", "v6", "v6_bf16", *OPERATOR_PARTS], default="",
                     help="measure this sub-record alone and print it (profiling)")
     ap.add_argument("--no-clocks", action="store_true")
     args = ap.parse_args(argv)

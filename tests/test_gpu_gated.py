@@ -346,3 +346,67 @@ def test_offsets_beyond_32_bits():
     x.copy_(torch.randn(1, T, C, device="cuda"))
     out, state = W.gated_forward(x, z)
     check_forward(x, z, None, "sigmoid", out, state)
+
+
+DEBUG_CHILD = r'''
+import numpy as np, torch, sys
+sys.path.insert(0, "tests")
+import wkv_recurrence_b200 as W
+from wkv_recurrence_b200 import _abi
+import test_gpu_gated as T
+assert _abi.LIB_PATH.endswith("libwkv_debug.so"), _abi.LIB_PATH
+checked = 0
+for (B, L, C) in ((2, 517, 200), (3, 129, 65), (1, 65, 36), (300, 140, 70), (1, 5000, 33)):
+    for xt, zt, ot in ((T.F32, T.F32, T.F32), (T.BF16, T.BF16, T.BF16), (T.BF16, T.F32, T.F32)):
+        for gate in ("sigmoid", "decay"):
+            x, z, h0 = T.draw(B, L, C, xt, zt, gate)
+            ws = torch.zeros(W.gated_workspace_size(B, L, C), dtype=torch.uint8, device="cuda")
+            marks = W.gated_checkpoints(x)
+            out, st = W.gated_forward(x, z, h0, gate=gate, out_dtype=ot, checkpoints=marks, workspace=ws)
+            g = torch.randn(B, L, C, device="cuda").to(ot)
+            got = W.gated_backward(x, z, g, h0, gate=gate, checkpoints=marks, workspace=ws)
+            assert W.query_status(ws) == 0, (B, L, C, xt, gate)
+            k = slice(0, 2)
+            T.check_forward(x[k], z[k], h0[k], gate, out[k], st[k])
+            T.check_backward(x[k], z[k], h0[k], g[k], None, gate, [t[k] for t in got])
+            checked += 1
+print("checked", checked)
+'''
+
+
+def test_bounds_checked_build():
+    import os
+    import subprocess
+    import sys
+
+    from wkv_recurrence_b200 import build
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    build.build(debug=True)
+    env = dict(os.environ, WKV_LIBRARY="debug", PYTHONPATH=root)
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD], cwd=root, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
+    assert "checked 30" in r.stdout
+
+
+def test_the_binding_refuses_on_the_gpu():
+    x = torch.zeros(2, 200, 8, device="cuda")
+    h = torch.zeros(2, 8, device="cuda")
+    bad = [(lambda: W.gated_forward(x, x[:, :5]), ValueError), (lambda: W.gated_forward(x[0], x[0]), ValueError),
+           (lambda: W.gated_forward(x.half(), x), TypeError), (lambda: W.gated_forward(x, x.bfloat16()), TypeError),
+           (lambda: W.gated_forward(x.transpose(1, 2), x.transpose(1, 2)), ValueError),
+           (lambda: W.gated_forward(x, x, gate="tanh"), ValueError), (lambda: W.gated_forward(x, x, gate=None), ValueError),
+           (lambda: W.gated_forward(x, x, h[:1]), ValueError), (lambda: W.gated_forward(x, x, h.double()), TypeError),
+           (lambda: W.gated_forward(x, x, h.cpu()), ValueError), (lambda: W.gated_forward(x, x, out_dtype=BF16), TypeError),
+           (lambda: W.gated_forward(x, x, out_dtype="f32"), TypeError),
+           (lambda: W.gated_forward(x, x, out=x[:, :, :4]), ValueError),
+           (lambda: W.gated_forward(x, x, checkpoints=torch.zeros(2, 1, 8, device="cuda")), ValueError),
+           (lambda: W.gated_forward(x, x, workspace=torch.zeros(300, dtype=torch.uint8)), ValueError),
+           (lambda: W.gated_backward(x, x, x.bfloat16()), TypeError), (lambda: W.gated_backward(x, x, x[:, :3]), ValueError),
+           (lambda: W.gated_backward(x, x, None), ValueError), (lambda: W.gated_step(h, x[:, 0], x[:, 0], out=h[:1]), ValueError),
+           (lambda: W.gated_step(None, x[:, 0], x[:, 0]), ValueError),
+           (lambda: W.gated_forward(x, x, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")), W.WkvError)]
+    for call, kind in bad:
+        with pytest.raises(kind):
+            call()
+    with pytest.raises(W.WkvError, match="wkv_gated_forward"):
+        bad[-1][0]()

@@ -266,3 +266,22 @@ def test_a_layer_of_them():
     # norms' r ~ 1 and summed over 400 rows for the weights
     for a, b in zip(got, want):
         assert float((a.double().cpu() - b).norm() / b.norm()) < 1e-5
+
+
+def test_the_binding_refuses_on_the_gpu():
+    x, w = torch.zeros(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    bad = [(lambda: W.rms_norm(x, w[:8]), ValueError), (lambda: W.rms_norm(x, w.bfloat16()), TypeError),
+           (lambda: W.rms_norm(x.half(), w), TypeError), (lambda: W.rms_norm(x, w.cpu()), ValueError),
+           (lambda: W.rms_norm(x, w, x[:2]), ValueError), (lambda: W.rms_norm(x, w, x.bfloat16()), TypeError),
+           (lambda: W.rms_norm(x, w, eps=0), ValueError), (lambda: W.rms_norm(x, w, eps=1e-60), ValueError),
+           (lambda: W.rms_norm(x, w, eps="a"), TypeError), (lambda: W.rms_norm(x, w, groups=3), ValueError),
+           (lambda: W.rms_norm(x, w, groups=0), ValueError), (lambda: W.rms_norm(x, w, out_dtype=BF16), TypeError),
+           (lambda: W.rms_norm(x, w, residual_out=x), ValueError), (lambda: W.rms_norm(x.t(), w[:4]), ValueError),
+           (lambda: W.rms_norm(torch.tensor(1.0, device="cuda"), w), ValueError),
+           (lambda: W.rms_norm_quant(x, w, block=16), ValueError), (lambda: W.rms_norm_quant(x, w, block=128), ValueError),
+           (lambda: W.rms_norm_backward(x, x.bfloat16(), w), TypeError), (lambda: W.rms_norm_backward(x[:2], x, w), ValueError),
+           (lambda: W.rms_norm_backward(x, x, w, x.bfloat16()), TypeError),
+           (lambda: W.rms_norm_backward(x, x, w, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda")), W.WkvError)]
+    for call, kind in bad:
+        with pytest.raises(kind):
+            call()
