@@ -60,14 +60,17 @@ Team fwd_team(int64_t D, bool vec) {
   return cta_team(n8, n8 <= 256 ? 1 : n8 <= 1024 ? 2 : n8 <= 2048 ? 4 : 8, !vec);
 }
 
-Team bwd_team(int64_t D, int64_t G, bool vec) {
+// s_bf: s (and gs, ds) in bf16. Then two vectors a thread fit beside the next
+// row's, and half as many warps meet at each row's barrier (65536 x 2048, gs:
+// 199 us with one, 181 with two; fp32 374 and 407).
+Team bwd_team(int64_t D, int64_t G, bool vec, bool s_bf) {
   const int64_t n8 = (D + 7) / 8;
   if (vec && n8 <= 64) {
     int tw = 4;
     while (tw < n8 && tw < 32) tw *= 2;
     if (tw * G <= 512) return Team{tw, n8 > 32 ? 2 : 1, 0, false};
   }
-  if (G == 1 && n8 <= 2048) return cta_team(n8, n8 <= 512 ? 1 : n8 <= 1024 ? 2 : 4, !vec);
+  if (G == 1 && n8 <= 2048) return cta_team(n8, n8 <= (s_bf && vec ? 96 : 512) ? 1 : n8 <= 1024 ? 2 : 4, !vec);
   return Team{0, 0, 0, false};
 }
 
@@ -78,9 +81,9 @@ struct BwdPlan {
 
 // vec: 16-byte aligned rows. Without a team (team.K = 0) the general kernels
 // run, on nparts parts of the rows.
-BwdPlan bwd_plan(int64_t N, int64_t C, int64_t G, bool vec) {
+BwdPlan bwd_plan(int64_t N, int64_t C, int64_t G, bool vec, bool s_bf) {
   BwdPlan pl;
-  pl.team = bwd_team(C / G, G, vec && (C / G) % 8 == 0);
+  pl.team = bwd_team(C / G, G, vec && (C / G) % 8 == 0, s_bf);
   pl.rpc = 1;
   pl.threads = pl.team.threads;
   if (!pl.team.K) {
@@ -98,11 +101,12 @@ BwdPlan bwd_plan(int64_t N, int64_t C, int64_t G, bool vec) {
   return pl;
 }
 
-// [parts][C] floats, then [N][G] for the general kernels: whichever a call's
-// alignment takes.
+// [parts][C] floats, then [N][G] for the general kernels: enough for whatever
+// a call's alignment and types take.
 size_t bwd_parts_bytes(int64_t N, int64_t C, int64_t G) {
   size_t most = 0;
-  for (const bool vec : {false, true}) most = std::max(most, (size_t)bwd_plan(N, C, G, vec).nparts);
+  for (const bool vec : {false, true})
+    for (const bool s_bf : {false, true}) most = std::max(most, (size_t)bwd_plan(N, C, G, vec, s_bf).nparts);
   return round_up(sizeof(float) * std::max<size_t>(most, 256) * (size_t)C, 256);
 }
 
@@ -359,7 +363,8 @@ wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps
   p.inv_d = 1.f / (float)p.D;
   const BwdPlan pl = bwd_plan(N, C, groups,
                               aligned(gy, 16) && rows_ok(sum, s_dtype, s_stride) && (!gsum || aligned(gsum, 16)) &&
-                                  aligned(dsum, 16) && aligned(weight, 16));
+                                  aligned(dsum, 16) && aligned(weight, 16),
+                              s_dtype == WKV_BF16);
   p.nparts = pl.nparts;
   if (pl.team.K) {
     bool ok;
