@@ -383,7 +383,9 @@ WKV_API wkv_status wkv_v6_forward(int64_t B, int64_t T, int64_t H, int64_t D,
  *                       token starts a sequence of its own (packed rows);
  *                       z = +inf keeps the state.
  *     WKV_GATE_DECAY    f = e^{-z}, i = 1 (z as wkv_ext's w_t; z = +inf
- *                       starts a sequence).
+ *                       starts a sequence). z < 0 lets the state grow; in
+ *                       contract while the product of f over any
+ *                       WKV_GATED_TILE tokens is finite in fp32.
  * NaN, and any other infinity, is out of contract. Like the WKV operators it
  * takes whole sequences with the state in and out, single tokens, and has a
  * backward.
@@ -541,7 +543,7 @@ WKV_API wkv_status wkv_forward_noalloc(int64_t B, int64_t T, int64_t C,
 
 /*
  * Synchronises `stream`, then reads and clears the device-side status word in
- * `workspace` (a wkv_forward, wkv_backward or wkv_v6_forward workspace).
+ * `workspace` (a wkv_forward, wkv_backward, wkv_v6_forward or gated workspace).
  * Returns WKV_OK, WKV_ERR_BOUNDS (bounds-checked build only), WKV_ERR_WAIT_TIMEOUT
  * if a device-side wait of an earlier call gave up (its outputs are then not
  * valid), or WKV_ERR_CUDA if the synchronisation itself failed.

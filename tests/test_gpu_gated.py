@@ -410,3 +410,53 @@ def test_the_binding_refuses_on_the_gpu():
             call()
     with pytest.raises(W.WkvError, match="wkv_gated_forward"):
         bad[-1][0]()
+
+
+FIRST_CALL_CHILD = r'''
+import torch, sys
+import wkv_recurrence_b200 as W
+x = torch.randn(2, 700, 96, device="cuda")
+g, w = torch.randn_like(x), torch.ones(96, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    marks = W.gated_checkpoints(x)
+    out, st = W.gated_forward(x, x, checkpoints=marks)
+    got = W.gated_backward(x, x, g, checkpoints=marks)
+    y, s = W.rms_norm(out, w, x)
+    ds, dw = W.rms_norm_backward(g, s, w)
+graph.replay()
+torch.cuda.synchronize()
+want, wst = W.gated_forward(x, x)
+assert torch.equal(out, want) and torch.equal(st, wst)
+assert all(torch.equal(a, b) for a, b in zip(got, W.gated_backward(x, x, g)))
+y2, s2 = W.rms_norm(want, w, x)
+d2, w2 = W.rms_norm_backward(g, s2, w)
+assert torch.equal(y, y2) and torch.equal(ds, d2) and torch.equal(dw, w2)
+print("the first call, captured")
+'''
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CHILD], cwd=root, env=dict(os.environ, PYTHONPATH=root),
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "the first call, captured" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """A workspace whose records cannot come (the header says that all tickets are taken but the first tiles' records are
+    missing) ends within the limit of each wait and says so."""
+    B, T, C = 1, 260, 64  # three tiles; the calls below take tickets 1, 2 and 3 (past the end)
+    ws = torch.zeros(W.gated_workspace_size(B, T, C), dtype=torch.uint8, device="cuda")
+    ws[:4].view(torch.int32).fill_(1)  # the ticket of tile 0 is gone: its total never arrives
+    x = torch.randn(B, T, C, device="cuda")
+    W.gated_forward(x, x, workspace=ws)
+    assert W.query_status(ws) == 6  # WKV_ERR_WAIT_TIMEOUT
+    assert W.query_status(ws) == 0
+    out, state = W.gated_forward(x, x, workspace=ws)  # the header is ready for the next call
+    assert W.query_status(ws) == 0
+    check_forward(x, x, None, "sigmoid", out, state)
