@@ -17,6 +17,7 @@
 #include <cuda_fp8.h>
 
 #include "wkv_device.cuh"
+#include "wkv_pair.cuh"
 
 namespace wkv {
 
@@ -39,9 +40,13 @@ struct Raw8<float, false> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
-  __device__ __forceinline__ static void store(float* p, int, int, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    a = make_float4(x[0], x[1], x[2], x[3]);
+    b = make_float4(x[4], x[5], x[6], x[7]);
+  }
+  __device__ __forceinline__ void put(float* p, int, int) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
   }
 };
 template <>
@@ -54,15 +59,14 @@ struct Raw8<__nv_bfloat16, false> {
     unpack_bf16x2(a.z, x[4], x[5]);
     unpack_bf16x2(a.w, x[6], x[7]);
   }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, int, int, const float (&x)[8]) {
-    uint4 o;
+  __device__ __forceinline__ void set(const float (&x)[8]) {  // rounded to nearest even
     __nv_bfloat162 t;
-    t = __floats2bfloat162_rn(x[0], x[1]), o.x = *reinterpret_cast<uint32_t*>(&t);
-    t = __floats2bfloat162_rn(x[2], x[3]), o.y = *reinterpret_cast<uint32_t*>(&t);
-    t = __floats2bfloat162_rn(x[4], x[5]), o.z = *reinterpret_cast<uint32_t*>(&t);
-    t = __floats2bfloat162_rn(x[6], x[7]), o.w = *reinterpret_cast<uint32_t*>(&t);
-    *reinterpret_cast<uint4*>(p) = o;
+    t = __floats2bfloat162_rn(x[0], x[1]), a.x = *reinterpret_cast<uint32_t*>(&t);
+    t = __floats2bfloat162_rn(x[2], x[3]), a.y = *reinterpret_cast<uint32_t*>(&t);
+    t = __floats2bfloat162_rn(x[4], x[5]), a.z = *reinterpret_cast<uint32_t*>(&t);
+    t = __floats2bfloat162_rn(x[6], x[7]), a.w = *reinterpret_cast<uint32_t*>(&t);
   }
+  __device__ __forceinline__ void put(__nv_bfloat16* p, int, int) const { *reinterpret_cast<uint4*>(p) = a; }
 };
 template <typename T>
 struct Raw8<T, true> {
@@ -75,12 +79,48 @@ struct Raw8<T, true> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = Elem<T>::to_f32(a[e]);
   }
-  __device__ __forceinline__ static void store(T* p, int st, int n, const float (&x)[8]) {
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = Elem<T>::from_f32(x[e]);
+  }
+  __device__ __forceinline__ void put(T* p, int st, int n) const {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (e < n) p[e * st] = Elem<T>::from_f32(x[e]);
+      if (e < n) p[e * st] = a[e];
   }
 };
+
+// x as T, rounded, to memory.
+template <typename T, bool SC>
+__device__ __forceinline__ void store8(T* p, int st, int n, const float (&x)[8]) {
+  Raw8<T, SC> r;
+  r.set(x);
+  r.put(p, st, n);
+}
+
+// sum + the squares, in two partial sums; products by one number and by eight.
+__device__ __forceinline__ float2 squares8(const float (&x)[8], float2 sum) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 v = make_float2(x[e], x[e + 1]);
+    sum = fma2(v, v, sum);
+  }
+  return sum;
+}
+__device__ __forceinline__ void scale8(float (&x)[8], float f) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 v = mul2(make_float2(x[e], x[e + 1]), splat(f));
+    x[e] = v.x, x[e + 1] = v.y;
+  }
+}
+__device__ __forceinline__ void scale8(float (&x)[8], const float (&w)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float2 v = mul2(make_float2(x[e], x[e + 1]), make_float2(w[e], w[e + 1]));
+    x[e] = v.x, x[e + 1] = v.y;
+  }
+}
 
 // The columns of vector k of team lane l, `width` lanes in the team.
 template <bool SC>
@@ -148,8 +188,12 @@ __device__ __forceinline__ float team_sum(float v) {
   for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float lanes_max(float v, int width) {  // over `width` (a power of two) adjacent lanes
-  for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+__device__ __forceinline__ float lanes_max(float v, int width) {  // over `width` (a power of two from 4) adjacent lanes
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  if (width > 4) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  if (width > 8) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  if (width > 16) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
   return v;
 }
 
@@ -206,7 +250,7 @@ __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams
     }
   }
   float s[K][kNV];
-  float sum = 0.f;
+  float2 sums = splat(0.f);
   const long long o = (long long)row * p.C + gc;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -217,16 +261,18 @@ __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams
         float r[kNV];
         rv[k].get(r);
 #pragma unroll
-        for (int e = 0; e < kNV; ++e) s[k][e] = Elem<R>::to_f32(Elem<R>::from_f32(s[k][e] + r[e]));
-        Raw8<R, SC>::store(static_cast<R*>(p.s) + o + c.at, c.st, c.n, s[k]);
+        for (int e = 0; e < kNV; ++e) s[k][e] += r[e];
+        rv[k].set(s[k]);  // the stream's rounding
+        rv[k].put(static_cast<R*>(p.s) + o + c.at, c.st, c.n);
+        rv[k].get(s[k]);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < kNV; ++e) s[k][e] = 0.f;
     }
-#pragma unroll
-    for (int e = 0; e < kNV; ++e) sum = fmaf(s[k][e], s[k][e], sum);
+    sums = squares8(s[k], sums);
   }
+  float sum = sums.x + sums.y;
   sum = TW ? team_sum<TW ? TW : 32>(sum) : cta_reduce<false>(sum, red);
   const float r = inv_root(fmaf(sum, p.inv_d, p.eps));
   const float* wp = p.weight + gc;
@@ -239,12 +285,11 @@ __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams
       float w[kNV];
       wv.load(wp + c.at, c.st, c.n);
       wv.get(w);
-      // in e4m3 r joins the scale: one product less per column
-#pragma unroll
-      for (int e = 0; e < kNV; ++e) s[k][e] = (f8 ? s[k][e] : s[k][e] * r) * w[e];
-      if (p.out_kind == kOutF32) Raw8<float, SC>::store(static_cast<float*>(p.y) + o + c.at, c.st, c.n, s[k]);
+      if (!f8) scale8(s[k], r);  // in e4m3 r joins the scale: one product less per column
+      scale8(s[k], w);
+      if (p.out_kind == kOutF32) store8<float, SC>(static_cast<float*>(p.y) + o + c.at, c.st, c.n, s[k]);
       if (p.out_kind == kOutBf16)
-        Raw8<__nv_bfloat16, SC>::store(static_cast<__nv_bfloat16*>(p.y) + o + c.at, c.st, c.n, s[k]);
+        store8<__nv_bfloat16, SC>(static_cast<__nv_bfloat16*>(p.y) + o + c.at, c.st, c.n, s[k]);
     }
   }
   if (!f8) return;
@@ -265,8 +310,7 @@ __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams
     const Cols<SC> c(k, tl, width, p.D);
     const float sc = e4m3_scale((whole ? all : lanes_max(top[k], per)) * r), f = r * rcp(sc);
     if (live && c.n > 0) {
-#pragma unroll
-      for (int e = 0; e < kNV; ++e) s[k][e] *= f;
+      scale8(s[k], f);
       store_e4m3<SC>(static_cast<unsigned char*>(p.y) + o + c.at, c.st, c.n, s[k]);
       if (whole ? k == 0 && tl == 0 : (tl & (per - 1)) == 0)
         p.scale[(long long)row * p.nb + (whole ? (uint32_t)gc / (uint32_t)p.block : (uint32_t)(gc + c.at) / (uint32_t)p.block)] = sc;
@@ -302,11 +346,13 @@ __global__ void __launch_bounds__(1024) wkv_norm_cross(const NormParams p, int r
       float r[kNV];
       rv.get(r);
 #pragma unroll
-      for (int e = 0; e < kNV; ++e) s[e] = Elem<R>::to_f32(Elem<R>::from_f32(s[e] + r[e]));
-      Raw8<R, false>::store(static_cast<R*>(p.s) + o, 1, kNV, s);
+      for (int e = 0; e < kNV; ++e) s[e] += r[e];
+      rv.set(s);
+      rv.put(static_cast<R*>(p.s) + o, 1, kNV);
+      rv.get(s);
     }
-#pragma unroll
-    for (int e = 0; e < kNV; ++e) sum = fmaf(s[e], s[e], sum);
+    const float2 sums = squares8(s, splat(0.f));
+    sum = sums.x + sums.y;
   }
   __syncthreads();  // tops is clear
   sum = team_sum<TW>(sum);
@@ -317,15 +363,16 @@ __global__ void __launch_bounds__(1024) wkv_norm_cross(const NormParams p, int r
     float w[kNV], m = 0.f;
     wv.load(p.weight + gc + c, 1, kNV);
     wv.get(w);
+    scale8(s, r);
+    scale8(s, w);
 #pragma unroll
-    for (int e = 0; e < kNV; ++e) s[e] = s[e] * r * w[e], m = fmaxf(m, fabsf(s[e]));
+    for (int e = 0; e < kNV; ++e) m = fmaxf(m, fabsf(s[e]));
     atomicMax(top, __float_as_int(m));  // bits of floats >= 0 are ordered as they are
   }
   __syncthreads();
   if (live) {
     const float sc = e4m3_scale(__int_as_float(*top)), f = rcp(sc);
-#pragma unroll
-    for (int e = 0; e < kNV; ++e) s[e] *= f;
+    scale8(s, f);
     store_e4m3<false>(static_cast<unsigned char*>(p.y) + o, 1, kNV, s);
     if ((uint32_t)(gc + c) % (uint32_t)p.block == 0) p.scale[row * p.nb + (uint32_t)(gc + c) / (uint32_t)p.block] = sc;
   }
@@ -454,7 +501,8 @@ template <typename Y, typename S, bool GS, int TW, int K, bool SC>
 __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, int rpc) {
   extern __shared__ float acc[];  // [C], TW > 0 with rpc > 1
   __shared__ float2 red[2][16];
-  constexpr bool kAhead = K <= 2;  // also: the weights stay in registers
+  constexpr bool kAhead = K <= 2;
+  constexpr bool kKeepW = K == 1 || (K == 2 && sizeof(S) == 2);  // weights in registers, else from L1
   const int tpr = TW ? TW * p.G : (int)blockDim.x;  // threads per row
   const int rl = TW ? (int)threadIdx.x / tpr : 0;   // row within the CTA's rpc rows
   const int tl = (int)threadIdx.x - rl * tpr;
@@ -463,7 +511,7 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
   const int width = TW ? TW : tpr;
   const bool lane_on = rl < rpc;
   const long long step = (long long)gridDim.x * rpc;
-  float dw[K][kNV], wk[kAhead ? K : 1][kNV];
+  float dw[K][kNV], wk[kKeepW ? K : 1][kNV];
   auto weights = [&](int k, float (&w)[kNV]) {
     const Cols<SC> c(k, l, width, p.D);
 #pragma unroll
@@ -478,7 +526,7 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
   for (int k = 0; k < K; ++k) {
 #pragma unroll
     for (int e = 0; e < kNV; ++e) dw[k][e] = 0.f;
-    if (kAhead) weights(k, wk[kAhead ? k : 0]);
+    if (kKeepW) weights(k, wk[kKeepW ? k : 0]);
   }
   Raw8<Y, SC> yv[K];
   Raw8<S, SC> sv[K], gv[K];
@@ -518,8 +566,8 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
 #pragma unroll
         for (int e = 0; e < kNV; ++e) s[k][e] = gy[k][e] = 0.f;
       }
-      float(&w)[kNV] = wk[kAhead ? k : 0];
-      if (!kAhead) weights(k, w);
+      float(&w)[kNV] = wk[kKeepW ? k : 0];
+      if (!kKeepW) weights(k, w);
 #pragma unroll
       for (int e = 0; e < kNV; ++e) {
         ss = fmaf(s[k][e], s[k][e], ss);
@@ -548,15 +596,15 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
       if (live && c.n > 0) {
         float d[kNV];
         if (GS) gv[k].get(d);
-        float(&w)[kNV] = wk[kAhead ? k : 0];
-        if (!kAhead) weights(k, w);
+        float(&w)[kNV] = wk[kKeepW ? k : 0];
+        if (!kKeepW) weights(k, w);
 #pragma unroll
         for (int e = 0; e < kNV; ++e) {
           const float t = gy[k][e] * w[e] - s[k][e] * m;
           d[e] = GS ? fmaf(r, t, d[e]) : r * t;
           dw[k][e] = fmaf(gy[k][e], s[k][e] * r, dw[k][e]);
         }
-        Raw8<S, SC>::store(static_cast<S*>(p.ds) + row * p.C + gc + c.at, c.st, c.n, d);
+        store8<S, SC>(static_cast<S*>(p.ds) + row * p.C + gc + c.at, c.st, c.n, d);
       }
     }
     if (kAhead) load_g(row + step);
@@ -574,7 +622,7 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
             if (!SC || e < c.n) dw[k][e] += acc[col + e * c.st];
         }
         if (turn == rpc - 1) {
-          Raw8<float, SC>::store(p.part + (long long)blockIdx.x * p.C + col, c.st, c.n, dw[k]);
+          store8<float, SC>(p.part + (long long)blockIdx.x * p.C + col, c.st, c.n, dw[k]);
         } else {
 #pragma unroll
           for (int e = 0; e < kNV; ++e)
