@@ -60,17 +60,21 @@ Team fwd_team(int64_t D, bool vec) {
   return cta_team(n8, n8 <= 256 ? 1 : n8 <= 1024 ? 2 : n8 <= 2048 ? 4 : 8, !vec);
 }
 
-// s_bf: s (and gs, ds) in bf16. Then two vectors a thread fit beside the next
-// row's, and half as many warps meet at each row's barrier (65536 x 2048, gs:
-// 199 us with one, 181 with two; fp32 374 and 407).
-Team bwd_team(int64_t D, int64_t G, bool vec, bool s_bf) {
+// s_bf: s (and gs, ds) in bf16; gs: the stream's own gradient is added. Two
+// vectors a thread keep more bytes under way and let half as many warps meet at
+// a row's barrier, where the registers hold them (65536 x 2048, gs: bf16 199 us
+// with one, 184 with two; fp32 376 and 310; 65536 x 12 x 64 bf16: 63 and 57).
+// fp32 without gs does better with one (32768 x 4096, gy bf16: 209 and 259).
+Team bwd_team(int64_t D, int64_t G, bool vec, bool s_bf, bool gs) {
   const int64_t n8 = (D + 7) / 8;
   if (vec && n8 <= 64) {
     int tw = 4;
     while (tw < n8 && tw < 32) tw *= 2;
-    if (tw * G <= 512) return Team{tw, n8 > 32 ? 2 : 1, 0, false};
+    const bool two = n8 > 32 || (s_bf && n8 > 4);
+    if (two && n8 <= 32) tw /= 2;
+    if (tw * G <= 512) return Team{tw, two ? 2 : 1, 0, false};
   }
-  if (G == 1 && n8 <= 2048) return cta_team(n8, n8 <= (s_bf && vec ? 96 : 512) ? 1 : n8 <= 1024 ? 2 : 4, !vec);
+  if (G == 1 && n8 <= 2048) return cta_team(n8, n8 <= (vec && (s_bf || gs) ? 96 : 512) ? 1 : n8 <= 1024 ? 2 : 4, !vec);
   return Team{0, 0, 0, false};
 }
 
@@ -81,9 +85,9 @@ struct BwdPlan {
 
 // vec: 16-byte aligned rows. Without a team (team.K = 0) the general kernels
 // run, on nparts parts of the rows.
-BwdPlan bwd_plan(int64_t N, int64_t C, int64_t G, bool vec, bool s_bf) {
+BwdPlan bwd_plan(int64_t N, int64_t C, int64_t G, bool vec, bool s_bf, bool gs) {
   BwdPlan pl;
-  pl.team = bwd_team(C / G, G, vec && (C / G) % 8 == 0, s_bf);
+  pl.team = bwd_team(C / G, G, vec && (C / G) % 8 == 0, s_bf, gs);
   pl.rpc = 1;
   pl.threads = pl.team.threads;
   if (!pl.team.K) {
@@ -105,8 +109,7 @@ BwdPlan bwd_plan(int64_t N, int64_t C, int64_t G, bool vec, bool s_bf) {
 // a call's alignment and types take.
 size_t bwd_parts_bytes(int64_t N, int64_t C, int64_t G) {
   size_t most = 0;
-  for (const bool vec : {false, true})
-    for (const bool s_bf : {false, true}) most = std::max(most, (size_t)bwd_plan(N, C, G, vec, s_bf).nparts);
+  for (int k = 0; k < 8; ++k) most = std::max(most, (size_t)bwd_plan(N, C, G, k & 1, k & 2, k & 4).nparts);
   return round_up(sizeof(float) * std::max<size_t>(most, 256) * (size_t)C, 256);
 }
 
@@ -271,11 +274,13 @@ bool resident(F fn, int threads, size_t smem, int* ctas) {
 
 template <typename Y, typename S, bool GS, int TW, int K, bool SC>
 bool bwd_launch(NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
-  const size_t smem = pl.rpc > 1 ? sizeof(float) * (size_t)p.C : 0;
+  int half = 0;  // the largest power of two below rpc, or 0
+  while (std::max(1, 2 * half) < pl.rpc) half = std::max(1, 2 * half);
+  const size_t smem = sizeof(float) * (size_t)half * p.C;
   int ctas;
   if (!resident(wkv_norm_bwd_team<Y, S, GS, TW, K, SC>, pl.threads, smem, &ctas)) return false;
   p.nparts = std::min(pl.nparts, ctas);
-  wkv_norm_bwd_team<Y, S, GS, TW, K, SC><<<(unsigned)p.nparts, pl.threads, smem, st>>>(p, pl.rpc);
+  wkv_norm_bwd_team<Y, S, GS, TW, K, SC><<<(unsigned)p.nparts, pl.threads, smem, st>>>(p, pl.rpc, half);
   return true;
 }
 
@@ -293,6 +298,9 @@ bool bwd_shape(NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
     case 8 * 8 + 1: return bwd_launch<Y, S, GS, 8, 1, false>(p, pl, st);
     case 16 * 8 + 1: return bwd_launch<Y, S, GS, 16, 1, false>(p, pl, st);
     case 32 * 8 + 1: return bwd_launch<Y, S, GS, 32, 1, false>(p, pl, st);
+    case 4 * 8 + 2: return bwd_launch<Y, S, GS, 4, 2, false>(p, pl, st);
+    case 8 * 8 + 2: return bwd_launch<Y, S, GS, 8, 2, false>(p, pl, st);
+    case 16 * 8 + 2: return bwd_launch<Y, S, GS, 16, 2, false>(p, pl, st);
     case 32 * 8 + 2: return bwd_launch<Y, S, GS, 32, 2, false>(p, pl, st);
     case 1: return bwd_launch<Y, S, GS, 0, 1, false>(p, pl, st);
     case 2: return bwd_launch<Y, S, GS, 0, 2, false>(p, pl, st);
@@ -364,7 +372,7 @@ wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps
   const BwdPlan pl = bwd_plan(N, C, groups,
                               aligned(gy, 16) && rows_ok(sum, s_dtype, s_stride) && (!gsum || aligned(gsum, 16)) &&
                                   aligned(dsum, 16) && aligned(weight, 16),
-                              s_dtype == WKV_BF16);
+                              s_dtype == WKV_BF16, gsum != nullptr);
   p.nparts = pl.nparts;
   if (pl.team.K) {
     bool ok;

@@ -495,11 +495,11 @@ struct NormBwdParams {
 // all threads (TW = 0, one group), K vectors of 8 columns per thread; SC as in
 // the forward. A thread keeps the same columns from row to row and adds up its
 // part of dweight in registers; the RPC rows' parts are joined through shared
-// memory at the end, in a fixed order. The next row is loaded while this one
+// memory at the end, pairwise. The next row is loaded while this one
 // is reduced (K <= 2: registers).
 template <typename Y, typename S, bool GS, int TW, int K, bool SC>
-__global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, int rpc) {
-  extern __shared__ float acc[];  // [C], TW > 0 with rpc > 1
+__global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, int rpc, int half) {
+  extern __shared__ float acc[];  // [half][C], half the largest power of two below rpc (0: rpc = 1)
   __shared__ float2 red[2][16];
   constexpr bool kAhead = K <= 2;
   constexpr bool kKeepW = K == 1 || (K == 2 && sizeof(S) == 2);  // weights in registers, else from L1
@@ -609,28 +609,33 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
     }
     if (kAhead) load_g(row + step);
   }
-  for (int turn = 0; turn < rpc; ++turn) {  // rows' parts join in order
-    if (turn == rl && lane_on) {
+  for (int h = half; h > 0; h >>= 1) {  // the rows' parts join pairwise, the upper half's onto the lower's
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const Cols<SC> c(k, l, width, p.D);
-        if (c.n <= 0) continue;
-        const int col = gc + c.at;
-        if (turn > 0) {
+    for (int k = 0; k < K; ++k) {
+      const Cols<SC> c(k, l, width, p.D);
+      if (lane_on && rl >= h && rl < 2 * h && c.n > 0) {
 #pragma unroll
-          for (int e = 0; e < kNV; ++e)
-            if (!SC || e < c.n) dw[k][e] += acc[col + e * c.st];
-        }
-        if (turn == rpc - 1) {
-          store8<float, SC>(p.part + (long long)blockIdx.x * p.C + col, c.st, c.n, dw[k]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kNV; ++e)
-            if (!SC || e < c.n) acc[col + e * c.st] = dw[k][e];
-        }
+        for (int e = 0; e < kNV; ++e)
+          if (!SC || e < c.n) acc[(rl - h) * p.C + gc + c.at + e * c.st] = dw[k][e];
       }
     }
-    if (rpc > 1) __syncthreads();
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const Cols<SC> c(k, l, width, p.D);
+      if (rl < h && rl + h < rpc && c.n > 0) {
+#pragma unroll
+        for (int e = 0; e < kNV; ++e)
+          if (!SC || e < c.n) dw[k][e] += acc[rl * p.C + gc + c.at + e * c.st];
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const Cols<SC> c(k, l, width, p.D);
+    if (lane_on && rl == 0 && c.n > 0)
+      store8<float, SC>(p.part + (long long)blockIdx.x * p.C + gc + c.at, c.st, c.n, dw[k]);
   }
 }
 
