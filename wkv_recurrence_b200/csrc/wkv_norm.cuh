@@ -510,6 +510,7 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
   const int l = TW ? tl % (TW ? TW : 1) : tl;
   const int width = TW ? TW : tpr;
   const bool lane_on = rl < rpc;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // wkv_norm_bwd_join may take its place and wait
   const long long step = (long long)gridDim.x * rpc;
   float dw[K][kNV], wk[kKeepW ? K : 1][kNV];
   auto weights = [&](int k, float (&w)[kNV]) {
@@ -692,6 +693,7 @@ __global__ void __launch_bounds__(1024) wkv_norm_bwd_join(const float* part, int
   __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   if (c < C) {
 #pragma unroll 8
     for (int i = w; i < nparts; i += 32) a += part[(long long)i * C + c];
