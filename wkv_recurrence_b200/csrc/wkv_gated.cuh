@@ -28,9 +28,16 @@
 // (the launch's number) vouches for its data without a fence, and a reader
 // polls the data itself.
 //
-// Bound: memory traffic (12 bytes per element fp32, 6 bf16; backward 20/10),
-// with instruction issue close behind: pairs of channels are computed with the
-// two-wide fp32 instructions.
+// Bound: memory traffic (12 bytes per element fp32, 6 bf16; backward 20/10) in
+// fp32, instruction issue in bf16 (55-60% of the slots are filled, 28
+// instructions per element forward and 54 backward); pairs of channels are
+// computed with the two-wide fp32 instructions, which took 14% off.
+//
+// Tile: 128 tokens by eight warps of 16, two CTAs per SM at 128 registers. What
+// a warp spends on a tile besides its tokens (copies' addresses, joining spans,
+// the chain) is about 250 instructions, so fewer, longer spans win as far as
+// registers hold them: 16 warps of 8 tokens, as many CTAs, took 532 us for the
+// 303 of 1 x 65536 x 2048 fp32 and 473 for the 340 of 16 x 4096 x 4096 bf16.
 #pragma once
 
 #include "wkv_device.cuh"
@@ -466,6 +473,10 @@ struct GatedShared {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
+// Measured (of the 6521 GB/s copy rate, for each input read and each output
+// written once): 1 x 65536 x 2048 fp32 303 us (0.81), 16 x 4096 x 4096 with
+// bf16 x and out and fp32 decays 354 us (0.93), all bf16 337 us (0.73; issue),
+// 8 x 1024 x 768 bf16 14.1 us (0.41: 2.6 rounds of tiles).
 template <typename X, typename Z, int J, int NW>
 constexpr size_t gated_fwd_smem() {
   return (size_t)J * NW * kGatedCG * (sizeof(X) + sizeof(Z));
@@ -589,6 +600,10 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
 // chain, and the states inside the tile are computed again from x and z.
 // x and z are fetched one tile ahead as soon as the states are done; g has two
 // buffers where both fit beside another CTA (kGB), else it is fetched last.
+//
+// Measured: 1 x 65536 x 2048 fp32 471 us (0.87), 16 x 4096 x 4096 bf16 with
+// fp32 decays 666 us (0.87), all bf16 615 us (0.67; issue), 8 x 1024 x 768
+// bf16 22.5 us (0.43).
 template <typename X, typename Z, typename O, int J, int NW>
 struct GatedBwdSmem {
   static constexpr size_t kRow = (size_t)J * NW * kGatedCG;
@@ -759,8 +774,9 @@ struct GatedStepParams {
   void* out;
 };
 
-// Elementwise and bound by memory (16 bytes per stream-channel in fp32, 14 in
-// bf16); V channels per thread move as 16-byte accesses of the state.
+// Elementwise and bound by memory (20 bytes per stream-channel in fp32, 14 in
+// bf16); four channels per thread move as 16-byte accesses of the state (4096 x
+// 768 bf16 8.2 us, 0.83 of the copy rate; eight per thread 8.4).
 template <typename X, typename Z, typename O, int GATE, int V>
 __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepParams p) {
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;

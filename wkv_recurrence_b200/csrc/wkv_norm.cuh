@@ -227,7 +227,12 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
 // scales here have their block inside a group: the whole group, or 32, 64 or
 // 128 columns held by adjacent lanes in one k.
 //
-// What a row costs beside its bytes is paid per thread (index, root, scale).
+// What a row costs beside its bytes is paid per thread (index, root, scale), so
+// wide rows have two vectors a thread and no divisions. Measured (of the 6521
+// GB/s copy rate): 65536 x 4096 bf16 with residual 311 us (1.06), in e4m3 by
+// 128 columns 274 us (1.05; 461 with one vector and IEEE divisions), e4m3
+// without a residual 166 us (0.74: issue, at 3 bytes a column); 65536 x 12 x 64
+// fp32 60 us (1.02); 40000 x 515 bf16 (SC) 49 us (0.51: 2-byte accesses).
 template <typename X, typename R, bool RES, int TW, int K, bool SC>
 __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams p) {
   __shared__ float red[32];
@@ -497,6 +502,10 @@ struct NormBwdParams {
 // part of dweight in registers; the RPC rows' parts are joined through shared
 // memory at the end, pairwise. The next row is loaded while this one
 // is reduced (K <= 2: registers).
+//
+// Measured: 65536 x 2048 bf16 with gs 180 us (0.91), fp32 310 us (1.06), 8191 x
+// 12 x 64 fp32 15.5 us of inputs out of L2 (0.74: a wave of 5 rows each, and
+// the parts' sum after it).
 template <typename Y, typename S, bool GS, int TW, int K, bool SC>
 __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, int rpc, int half) {
   extern __shared__ float acc[];  // [half][C], half the largest power of two below rpc (0: rpc = 1)
