@@ -113,6 +113,15 @@ def test_rows_and_blocks_of_zeros():
     # a row whose y is far below fp32's smallest normal number still has a finite inverse scale
     q, scale, _ = W.rms_norm_quant(torch.full((1, 64), 1e-38, device="cuda"), torch.full((64,), 1e-6, device="cuda"), eps=1.0)
     assert bool(scale.isfinite().all()) and bool((q.float() >= 0).all()) and float(scale) >= 1.17549435e-38
+    # nor do zeros beside such values become anything else (1 / sqrt(eps) = 1000 on top of that inverse)
+    x = torch.zeros(1, 64, device="cuda")
+    x[0, ::2] = 2e-38
+    for C in (64, 63):
+        q, scale, _ = W.rms_norm_quant(x[:, :C].contiguous(), torch.full((C,), 1e-3, device="cuda"))
+        assert bool((q.float()[0, 1::2] == 0).all()) and bool((q.float()[0, ::2] > 0).all())
+    # squares that overflow: the norm is 0, as the formula's in fp32
+    y, _ = W.rms_norm(torch.full((1, 64), 1e20, device="cuda"), torch.ones(64, device="cuda"))
+    assert torch.equal(y, torch.zeros_like(y))
 
 
 @pytest.mark.parametrize("N,C,groups", SIZES + [(700, 768, 12), (3001, 96, 1), (1500, 2048, 1), (400, 100, 5)])

@@ -195,9 +195,8 @@ __device__ __forceinline__ void copy_rows(T* dst, const T* src, const T* safe, l
 
 // A warp's J rows of 64 channels into shared memory: `rows` rows and `left`
 // channels exist from `src` on, the others are zeros (`safe`: an address for
-// copies of nothing). gran: bytes that base, strides and
-// row length are multiples of (16, 4, or 2: an element of bf16, copied through
-// registers).
+// copies of nothing). gran: bytes that base, strides and row length are
+// multiples of (16, 4, or 2: an element of bf16, copied through registers).
 template <typename T, int J>
 __device__ __forceinline__ void copy_span(T* dst, const T* src, const T* safe, long long st, int rows, int left, int gran) {
   if (gran == 16) {
@@ -248,9 +247,9 @@ __device__ __forceinline__ bool rec_load(const GatedRec* r, uint64_t tag, float&
 
 constexpr uint64_t kGatedTag = 0x47415445ull << 32;  // tag = kGatedTag + the launch's number on this workspace
 
-// t / d for t < 2^31 as a product: m = ceil(2^sh / d) with sh = 31 + ceil(log2
-// d) exceeds 2^sh / d by less than one, which t / 2^31 < 1 of a unit in the
-// quotient's 2^-ceil(log2 d) cannot reach.
+// t / d for t < 2^31 as floor(t m / 2^sh), sh = 31 + ceil(log2 d): m = ceil(2^sh
+// / d) is less than 1 too large, so t m / 2^sh less than t / 2^sh < 1 / d, the
+// least distance of t / d from the next whole number.
 struct Divisor {
   uint32_t d, m;
   int sh;
@@ -345,8 +344,8 @@ struct Head {
 __device__ __forceinline__ const GatedRec* head_rec(const GatedParams& p, int item, int pos) {
   return p.pre + ((size_t)item * p.ngrp + pos / p.G - 1) * kGatedCG + (threadIdx.x & 31) * 2;
 }
-__device__ __forceinline__ Head head_ask(const GatedParams& p, int item, int pos, uint64_t tag, float2 first) {
-  Head r{first, true};
+__device__ __forceinline__ Head head_ask(const GatedParams& p, int item, int pos, uint64_t tag) {
+  Head r{splat(0.f), true};
   if (p.G == 1 && pos > 0) {
     float P;
     const GatedRec* rec = head_rec(p, item, pos);
@@ -355,7 +354,8 @@ __device__ __forceinline__ Head head_ask(const GatedParams& p, int item, int pos
   }
   return r;
 }
-__device__ __forceinline__ float2 head_get(const GatedParams& p, int item, int pos, uint64_t tag, Head r) {
+__device__ __forceinline__ float2 head_get(const GatedParams& p, int item, int pos, uint64_t tag, float2 first, Head r) {
+  if (pos == 0) return first;
   if (!r.got) {
     float2 P;
     rec_wait(head_rec(p, item, pos), tag, P, r.H, p);
@@ -466,6 +466,7 @@ struct GatedShared {
   Span agg[2][NWMAX][32];   // the warps' spans, by parity of the tile
   float2 rev[2][NWMAX][32];  // backward: their gradients (the P is the same)
   Front<NWMAX> front;
+  float2 first[2][32];      // by parity: the state (gradient) before the sequence, of a tile that starts it
   long long next[2];        // by parity: the ticket after this one
   uint32_t epoch;
 };
@@ -520,12 +521,11 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     const int nt = p.T - t0;  // tokens from this span on
     const int c0 = a.cg + lane * 2;
     if (threadIdx.x == 0) ticket = gated_ticket(p, ticket);
-    // The state before the sequence enters the scan at its first tile alone:
-    // its total, which carries it on, depends on this load, so h_out may be
-    // h0. (In a single tile the barrier below stands between this load and
-    // that store.)
-    const float2 first = p.h0 && a.pos == 0 ? row_get(p.h0, (long long)a.b * p.C, c0, p.C) : splat(0.f);
-    const Head ask = head_ask(p, a.item, a.pos, tag, first);
+    // The state before the sequence enters the scan at its first tile alone, by
+    // one warp, and is in shared memory before the barrier: whatever the tile
+    // hands on lies behind this load, so h_out may be h0.
+    if (w == 0 && a.pos == 0) sh.first[par][lane] = p.h0 ? row_get(p.h0, (long long)a.b * p.C, c0, p.C) : splat(0.f);
+    const Head ask = head_ask(p, a.item, a.pos, tag);
 
     copy_wait();
     __syncwarp();
@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     const Tile an = gated_tile(p, sh.next[par]);
     fetch(an);  // every lane's reads of the tile lie before the barrier
 
+    const float2 first = a.pos == 0 ? sh.first[par][lane] : splat(0.f);
     float2 h;  // the state in front of the tile
     if (chained && p.G > 1) {
       h = gated_front<NWMAX>(p, a.item, a.pos, tag, first, sh.front, [&] {
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
         return tot;
       });
     } else {
-      h = head_get(p, a.item, a.pos, tag, ask);
+      h = head_get(p, a.item, a.pos, tag, first, ask);
     }
     if (p.marks && w == 0)
       row_put(p.hdr, p.marks, ((long long)a.b * p.nch + a.pos) * p.C, c0, p.C, (size_t)p.B * p.nch * p.C, h);
@@ -662,12 +663,13 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     const int c0 = a.cg + lane * 2;
     O* sg = sg0 + (kGB == 2 && par ? row : 0);
     if (threadIdx.x == 0) ticket = gated_ticket(p, ticket);
-    // gradient behind the sequence (it enters at the scan's first tile alone,
-    // as in the forward), state in front of the tile
-    const float2 first = p.dh_out && a.pos == 0 ? row_get(p.dh_out, (long long)a.b * p.C, c0, p.C) : splat(0.f);
+    // gradient behind the sequence (as the state in the forward: dh0 may be
+    // dh_out), state in front of the tile
+    if (w == 0 && a.pos == 0)
+      sh.first[par][lane] = p.dh_out ? row_get(p.dh_out, (long long)a.b * p.C, c0, p.C) : splat(0.f);
     float2 h = chained ? row_get(p.marks, ((long long)a.b * p.nch + chunk) * p.C, c0, p.C)
                        : (p.h0 ? row_get(p.h0, (long long)a.b * p.C, c0, p.C) : splat(0.f));
-    const Head ask = head_ask(p, a.item, a.pos, tag, first);
+    const Head ask = head_ask(p, a.item, a.pos, tag);
 
     copy_wait();
     __syncwarp();
@@ -705,6 +707,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     fetch_xz(an);
     if (kGB == 2) fetch_g(an, sg0 + (par ? 0 : row));
     copy_commit();
+    const float2 first = a.pos == 0 ? sh.first[par][lane] : splat(0.f);
     float2 q;  // f_{t+1} D_{t+1}, what flows back into token t
     if (chained && p.G > 1) {
       q = gated_front<NWMAX>(p, a.item, a.pos, tag, first, sh.front, [&] {
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
         return tot;
       });
     } else {
-      q = head_get(p, a.item, a.pos, tag, ask);
+      q = head_get(p, a.item, a.pos, tag, first, ask);
     }
     for (int i = NW - 1; i > w; --i) q = fma2(sh.agg[par][i][lane].P, q, sh.rev[par][i][lane]);
     if (chained && p.G == 1 && w == 0 && a.pos != p.nch - 1)

@@ -133,10 +133,11 @@ struct Cols {
   }
 };
 
-// (v + eps)^-1/2: the approximation and one Newton step
+// v^-1/2: the approximation and one Newton step (not for a sum that
+// overflowed: 0 there)
 __device__ __forceinline__ float inv_root(float v) {
   const float r = rsqrtf(v);
-  return fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r);
+  return v <= 3.4028235e38f ? fmaf(0.5f * r, fmaf(-v * r, r, 1.f), r) : r;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -313,9 +314,14 @@ __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const Cols<SC> c(k, tl, width, p.D);
-    const float sc = e4m3_scale((whole ? all : lanes_max(top[k], per)) * r), f = r * rcp(sc);
+    const float sc = e4m3_scale((whole ? all : lanes_max(top[k], per)) * r), inv = rcp(sc);
     if (live && c.n > 0) {
-      scale8(s[k], f);
+      if (sc < 1e-30f) {  // r / sc might overflow
+        scale8(s[k], r);
+        scale8(s[k], inv);
+      } else {
+        scale8(s[k], r * inv);
+      }
       store_e4m3<SC>(static_cast<unsigned char*>(p.y) + o + c.at, c.st, c.n, s[k]);
       if (whole ? k == 0 && tl == 0 : (tl & (per - 1)) == 0)
         p.scale[(long long)row * p.nb + (whole ? (uint32_t)gc / (uint32_t)p.block : (uint32_t)(gc + c.at) / (uint32_t)p.block)] = sc;
