@@ -192,7 +192,7 @@ def source_digest() -> str:
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "wkv_recurrence_b200", "csrc")
     for p in sorted(glob.glob(os.path.join(csrc, "*.cuh")) + glob.glob(os.path.join(csrc, "*.cu"))):
-        if os.path.basename(p).startswith(("wkv_gated.", "wkv_norm.")):
+        if os.path.basename(p).startswith(("wkv_gated.", "wkv_norm.", "wkv_pair.")):
             continue
         with open(p, "rb") as f:
             h.update(os.path.basename(p).encode())
