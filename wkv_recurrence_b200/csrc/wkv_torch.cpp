@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -114,8 +115,10 @@ const Tensor& exact(PyObject* o, const char* name, c10::Device dev, at::IntArray
   if (!t.is_contiguous()) bad_value(std::string(name) + " must be contiguous");
   return t;
 }
+// From torch's allocator without its dispatcher (a third of the call's time
+// would go into finding that a CUDA tensor is wanted).
 Tensor fresh(c10::Device dev, at::IntArrayRef shape, ScalarType type) {
-  return at::empty(shape, at::TensorOptions().device(dev).dtype(type));
+  return Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
 // The tensor passed, checked, or a new one.
 Tensor result(PyObject* o, const char* name, c10::Device dev, at::IntArrayRef shape, ScalarType type) {
