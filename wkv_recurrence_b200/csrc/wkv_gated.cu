@@ -112,8 +112,7 @@ struct FwdLaunch {
     // a single tile of fewer warps takes less shared memory: more CTAs fit
     const size_t smem = gated_fwd_smem<X, Z, kGatedJ, kGatedNW>() / kGatedNW * pl.NW;
     const long long most = (long long)ctas * (kGatedNW / pl.NW);
-    fn<<<(unsigned)std::min(pl.tiles, most), 32 * pl.NW, smem, st>>>(p);
-    return launch_result();
+    return launch_follow_on(fn, (unsigned)std::min(pl.tiles, most), 32 * pl.NW, smem, st, p);
   }
 };
 struct BwdLaunch {
@@ -126,8 +125,7 @@ struct BwdLaunch {
     if (!resident(r, fn, 32 * kGatedNW, Smem::kBytes, &ctas)) return WKV_ERR_CUDA;
     const size_t smem = Smem::kBytes / kGatedNW * pl.NW;
     const long long most = (long long)ctas * (kGatedNW / pl.NW);
-    fn<<<(unsigned)std::min(pl.tiles, most), 32 * pl.NW, smem, st>>>(p);
-    return launch_result();
+    return launch_follow_on(fn, (unsigned)std::min(pl.tiles, most), 32 * pl.NW, smem, st, p);
   }
 };
 
@@ -150,11 +148,11 @@ template <typename X, typename Z, typename O>
 wkv_status step_launch(int gate, int V, const GatedStepParams& p, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.n + 255) / 256);
   if (gate == WKV_GATE_SIGMOID) {
-    if (V == 4) gated_step_kernel<X, Z, O, kGateSigmoid, 4><<<grid, 256, 0, st>>>(p);
-    else gated_step_kernel<X, Z, O, kGateSigmoid, 1><<<grid, 256, 0, st>>>(p);
+    if (V == 4) return launch_follow_on(gated_step_kernel<X, Z, O, kGateSigmoid, 4>, grid, 256, 0, st, p);
+    else return launch_follow_on(gated_step_kernel<X, Z, O, kGateSigmoid, 1>, grid, 256, 0, st, p);
   } else {
-    if (V == 4) gated_step_kernel<X, Z, O, kGateDecay, 4><<<grid, 256, 0, st>>>(p);
-    else gated_step_kernel<X, Z, O, kGateDecay, 1><<<grid, 256, 0, st>>>(p);
+    if (V == 4) return launch_follow_on(gated_step_kernel<X, Z, O, kGateDecay, 4>, grid, 256, 0, st, p);
+    else return launch_follow_on(gated_step_kernel<X, Z, O, kGateDecay, 1>, grid, 256, 0, st, p);
   }
   return launch_result();
 }

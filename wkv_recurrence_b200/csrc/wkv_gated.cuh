@@ -485,6 +485,7 @@ constexpr size_t gated_fwd_smem() {
 
 template <typename X, typename Z, typename O, int GATE, int J, int NWMAX>
 __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const GatedParams p) {
+  follow_on();
   using Gt = Gate<GATE>;
   extern __shared__ __align__(16) unsigned char tiles[];
   __shared__ GatedShared<NWMAX> sh;
@@ -614,6 +615,7 @@ struct GatedBwdSmem {
 
 template <typename X, typename Z, typename O, int GATE, int J, int NWMAX>
 __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const GatedParams p) {
+  follow_on();
   using Gt = Gate<GATE>;
   constexpr int kGB = GatedBwdSmem<X, Z, O, J, NWMAX>::kGB;
   extern __shared__ __align__(16) unsigned char tiles[];
@@ -782,6 +784,7 @@ struct GatedStepParams {
 // 768 bf16 8.2 us, 0.83 of the copy rate; eight per thread 8.4).
 template <typename X, typename Z, typename O, int GATE, int V>
 __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepParams p) {
+  follow_on();
   const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= p.n) return;
   long long s;

@@ -114,14 +114,14 @@ size_t bwd_parts_bytes(int64_t N, int64_t C, int64_t G) {
 }
 
 template <typename X, typename R, bool RES, int TW, int K, bool SC = false>
-void launch_team(const NormParams& p, int threads, cudaStream_t st) {
+wkv_status launch_team(const NormParams& p, int threads, cudaStream_t st) {
   const long long segs = p.N * p.G;
   const unsigned grid = (unsigned)(TW ? (segs * TW + 255) / 256 : segs);
-  wkv_norm_team<X, R, RES, TW, K, SC><<<grid, threads, 0, st>>>(p);
+  return launch_follow_on(wkv_norm_team<X, R, RES, TW, K, SC>, grid, (unsigned)threads, 0, st, p);
 }
 
 template <typename X, typename R, bool RES>
-void fwd_shape(const NormParams& p, const Team& t, cudaStream_t st) {
+wkv_status fwd_shape(const NormParams& p, const Team& t, cudaStream_t st) {
   if (t.sc) {
     switch (t.K) {
       case 1: return launch_team<X, R, RES, 0, 1, true>(p, t.threads, st);
@@ -156,21 +156,20 @@ int cross_lanes(int64_t D, int64_t G) {
 }
 
 template <typename X, typename R, bool RES>
-void cross_shape(const NormParams& p, int tw, cudaStream_t st) {
+wkv_status cross_shape(const NormParams& p, int tw, cudaStream_t st) {
   const int tpr = tw * p.G, rpc = std::max(1, 256 / tpr);
   const unsigned grid = (unsigned)((p.N + rpc - 1) / rpc);
   const int threads = (int)round_up((size_t)rpc * tpr, 32);
   const size_t smem = sizeof(int) * (size_t)rpc * p.nb;
-  if (tw == 4) wkv_norm_cross<X, R, RES, 4><<<grid, threads, smem, st>>>(p, rpc);
-  else if (tw == 8) wkv_norm_cross<X, R, RES, 8><<<grid, threads, smem, st>>>(p, rpc);
-  else if (tw == 16) wkv_norm_cross<X, R, RES, 16><<<grid, threads, smem, st>>>(p, rpc);
-  else wkv_norm_cross<X, R, RES, 32><<<grid, threads, smem, st>>>(p, rpc);
+  if (tw == 4) return launch_follow_on(wkv_norm_cross<X, R, RES, 4>, grid, (unsigned)threads, smem, st, p, rpc);
+  else if (tw == 8) return launch_follow_on(wkv_norm_cross<X, R, RES, 8>, grid, (unsigned)threads, smem, st, p, rpc);
+  else if (tw == 16) return launch_follow_on(wkv_norm_cross<X, R, RES, 16>, grid, (unsigned)threads, smem, st, p, rpc);
+  else return launch_follow_on(wkv_norm_cross<X, R, RES, 32>, grid, (unsigned)threads, smem, st, p, rpc);
 }
 
 template <typename X, typename R, bool RES>
-void fwd_launch(const NormParams& p, const Team& t, int cross, cudaStream_t st) {
-  if (cross) cross_shape<X, R, RES>(p, cross, st);
-  else fwd_shape<X, R, RES>(p, t, st);
+wkv_status fwd_launch(const NormParams& p, const Team& t, int cross, cudaStream_t st) {
+  return cross ? cross_shape<X, R, RES>(p, cross, st) : fwd_shape<X, R, RES>(p, t, st);
 }
 
 // A general row kernel may use 48 KB of shared memory without asking.
@@ -229,19 +228,12 @@ wkv_status norm(int64_t N, int64_t C, int64_t G, float eps, const void* x, int x
   // narrow groups of rows that are not aligned: a CTA each is a waste
   if (t.sc && t.threads < 64 && G > 1) t.K = 0;
   if ((t.K || cross) && N * G < (1ll << 31)) {
-    if (!res) {
-      if (x_dtype == WKV_F32) fwd_launch<float, float, false>(p, t, cross, st);
-      else fwd_launch<bf, bf, false>(p, t, cross, st);
-    } else if (x_dtype == WKV_F32) {
-      fwd_launch<float, float, true>(p, t, cross, st);
-    } else if (r_dtype == WKV_F32) {
-      fwd_launch<bf, float, true>(p, t, cross, st);
-    } else {
-      fwd_launch<bf, bf, true>(p, t, cross, st);
-    }
-  } else {
-    wkv_norm_row<<<(unsigned)N, 256, sizeof(float) * (size_t)G, st>>>(p, x_dtype == WKV_BF16, r_dtype == WKV_BF16);
+    if (!res)
+      return x_dtype == WKV_F32 ? fwd_launch<float, float, false>(p, t, cross, st) : fwd_launch<bf, bf, false>(p, t, cross, st);
+    if (x_dtype == WKV_F32) return fwd_launch<float, float, true>(p, t, cross, st);
+    return r_dtype == WKV_F32 ? fwd_launch<bf, float, true>(p, t, cross, st) : fwd_launch<bf, bf, true>(p, t, cross, st);
   }
+  wkv_norm_row<<<(unsigned)N, 256, sizeof(float) * (size_t)G, st>>>(p, x_dtype == WKV_BF16, r_dtype == WKV_BF16);
   return launch_result();
 }
 
@@ -280,8 +272,8 @@ bool bwd_launch(NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
   int ctas;
   if (!resident(wkv_norm_bwd_team<Y, S, GS, TW, K, SC>, pl.threads, smem, &ctas)) return false;
   p.nparts = std::min(pl.nparts, ctas);
-  wkv_norm_bwd_team<Y, S, GS, TW, K, SC><<<(unsigned)p.nparts, pl.threads, smem, st>>>(p, pl.rpc, half);
-  return true;
+  return launch_follow_on(wkv_norm_bwd_team<Y, S, GS, TW, K, SC>, (unsigned)p.nparts, (unsigned)pl.threads, smem, st, p,
+                          pl.rpc, half) == WKV_OK;
 }
 
 template <typename Y, typename S, bool GS>
@@ -390,19 +382,8 @@ wkv_status wkv_rms_norm_backward(int64_t N, int64_t C, int64_t groups, float eps
                                                                                              s_dtype == WKV_BF16);
   }
   if (launch_result() != WKV_OK) return WKV_ERR_CUDA;
-  // launched while the parts are still being written; it waits for them on the
-  // device (8191 x 12 x 64 fp32: 16.5 us without, 15.6 with)
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((C + 31) / 32));
-  cfg.blockDim = dim3(1024);
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  const float* part = p.part;
-  return cuda_ok(cudaLaunchKernelEx(&cfg, wkv_norm_bwd_join, part, p.nparts, p.C, dweight)) ? WKV_OK : WKV_ERR_CUDA;
+  return launch_follow_on(wkv_norm_bwd_join, (unsigned)((C + 31) / 32), 1024, 0, st, (const float*)p.part, p.nparts, p.C,
+                          dweight);
 }
 
 }  // extern "C"

@@ -236,6 +236,7 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
 // fp32 60 us (1.02); 40000 x 515 bf16 (SC) 49 us (0.51: 2-byte accesses).
 template <typename X, typename R, bool RES, int TW, int K, bool SC>
 __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams p) {
+  follow_on();
   __shared__ float red[32];
   const int width = TW ? TW : (int)blockDim.x;
   const int tl = TW ? (int)(threadIdx.x % width) : (int)threadIdx.x;
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams
 // (the order of maxima does not matter).
 template <typename X, typename R, bool RES, int TW>
 __global__ void __launch_bounds__(1024) wkv_norm_cross(const NormParams p, int rpc) {
+  follow_on();
   extern __shared__ int tops[];  // [rpc][nb]
   const int tpr = TW * p.G;
   const int rl = (int)threadIdx.x / tpr, tl = (int)threadIdx.x - rl * tpr;
@@ -514,6 +516,7 @@ struct NormBwdParams {
 // the parts' sum after it).
 template <typename Y, typename S, bool GS, int TW, int K, bool SC>
 __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, int rpc, int half) {
+  follow_on();
   extern __shared__ float acc[];  // [half][C], half the largest power of two below rpc (0: rpc = 1)
   __shared__ float2 red[2][16];
   constexpr bool kAhead = K <= 2;
@@ -525,7 +528,6 @@ __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, 
   const int l = TW ? tl % (TW ? TW : 1) : tl;
   const int width = TW ? TW : tpr;
   const bool lane_on = rl < rpc;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // wkv_norm_bwd_join may take its place and wait
   const long long step = (long long)gridDim.x * rpc;
   float dw[K][kNV], wk[kKeepW ? K : 1][kNV];
   auto weights = [&](int k, float (&w)[kNV]) {
@@ -705,10 +707,10 @@ __global__ void __launch_bounds__(256) wkv_norm_bwd_cols(const NormBwdParams p, 
 // dweight = the parts' sum, in a fixed order: of 32 columns, each of 32 warps
 // adds every 32nd part, then a warp joins the 32 sums of a column.
 __global__ void __launch_bounds__(1024) wkv_norm_bwd_join(const float* part, int nparts, int C, float* dw) {
+  follow_on();
   __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   if (c < C) {
 #pragma unroll 8
     for (int i = w; i < nparts; i += 32) a += part[(long long)i * C + c];

@@ -1,8 +1,17 @@
-// Arithmetic on pairs of fp32 numbers with the two-wide instructions of
-// sm_100a (fma, mul and add on f32x2): one issue slot for two results.
+// Shared by the gated recurrence and the norm: the start of a kernel that may
+// be launched early, and arithmetic on pairs of fp32 numbers with the two-wide
+// instructions of sm_100a (fma, mul and add on f32x2): one issue slot for two
+// results.
 #pragma once
 
 namespace wkv {
+
+// First statement of a kernel launched by launch_follow_on: lets the next such
+// kernel take its places as these become free, and waits until the kernel
+// before has ended and its writes can be read.
+__device__ __forceinline__ void follow_on() {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
