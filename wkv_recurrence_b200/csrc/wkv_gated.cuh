@@ -475,9 +475,9 @@ struct GatedShared {
 // forward
 // ---------------------------------------------------------------------------
 // Measured (of the 6521 GB/s copy rate, for each input read and each output
-// written once): 1 x 65536 x 2048 fp32 303 us (0.81), 16 x 4096 x 4096 with
-// bf16 x and out and fp32 decays 354 us (0.93), all bf16 337 us (0.73; issue),
-// 8 x 1024 x 768 bf16 14.1 us (0.41: 2.6 rounds of tiles).
+// written once): 1 x 65536 x 2048 fp32 304 us (0.81), 16 x 4096 x 4096 with
+// bf16 x and out and fp32 decays 343 us (0.96), all bf16 344 us (0.72; issue),
+// 8 x 1024 x 768 bf16 14.3 us (0.41: 2.6 rounds of tiles).
 template <typename X, typename Z, int J, int NW>
 constexpr size_t gated_fwd_smem() {
   return (size_t)J * NW * kGatedCG * (sizeof(X) + sizeof(Z));
@@ -604,8 +604,8 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
 // buffers where both fit beside another CTA (kGB), else it is fetched last.
 //
 // Measured: 1 x 65536 x 2048 fp32 471 us (0.87), 16 x 4096 x 4096 bf16 with
-// fp32 decays 666 us (0.87), all bf16 615 us (0.67; issue), 8 x 1024 x 768
-// bf16 22.5 us (0.43).
+// fp32 decays 624-660 us (0.87-0.92), all bf16 617 us (0.67; issue), 8 x 1024 x
+// 768 bf16 22.1 us (0.44).
 template <typename X, typename Z, typename O, int J, int NW>
 struct GatedBwdSmem {
   static constexpr size_t kRow = (size_t)J * NW * kGatedCG;
@@ -780,8 +780,9 @@ struct GatedStepParams {
 };
 
 // Elementwise and bound by memory (20 bytes per stream-channel in fp32, 14 in
-// bf16); four channels per thread move as 16-byte accesses of the state (4096 x
-// 768 bf16 8.2 us, 0.83 of the copy rate; eight per thread 8.4).
+// bf16); four channels per thread move as 16-byte accesses of the state. Steps
+// of 4096 x 768 bf16, one after the other: 6.7 us (1.0 of the copy rate; 8.2
+// each waiting for its launch).
 template <typename X, typename Z, typename O, int GATE, int V>
 __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepParams p) {
   follow_on();

@@ -512,8 +512,8 @@ struct NormBwdParams {
 // is reduced (K <= 2: registers).
 //
 // Measured: 65536 x 2048 bf16 with gs 180 us (0.91), fp32 310 us (1.06), 8191 x
-// 12 x 64 fp32 15.5 us of inputs out of L2 (0.74: a wave of 5 rows each, and
-// the parts' sum after it).
+// 12 x 64 fp32 15.4 us of inputs out of L2 (0.75: one wave of nine turns a CTA,
+// and the parts' sum behind it).
 template <typename Y, typename S, bool GS, int TW, int K, bool SC>
 __global__ void __launch_bounds__(512) wkv_norm_bwd_team(const NormBwdParams p, int rpc, int half) {
   follow_on();
