@@ -294,3 +294,39 @@ def test_the_binding_refuses_on_the_gpu():
     for call, kind in bad:
         with pytest.raises(kind):
             call()
+
+
+@pytest.mark.parametrize("S,C", [(3, 64), (700, 768), (4096, 1024)])
+def test_a_chain_of_calls_is_ordered(S, C):
+    """Each call reads what the one before wrote, in place where that is allowed, with nothing between them: the kernels
+    are launched before their predecessors end, and must not read before. The same calls with a wait between give the
+    same bits."""
+    g = torch.Generator(device="cuda").manual_seed(S)
+    x0 = torch.randn(S, C, generator=g, device="cuda")
+    w = 1 + 0.1 * torch.randn(C, generator=g, device="cuda")
+    gates = torch.randn(S, C, generator=g, device="cuda")
+
+    def run(wait):
+        def after(*r):
+            if wait:
+                torch.cuda.synchronize()
+            return r
+
+        x, res, state = x0.clone(), x0.clone(), torch.zeros(S, C, device="cuda")
+        kept = []
+        for _ in range(12):
+            y, res = after(*W.rms_norm(x, w, res, residual_out=res))
+            x, state = after(*W.gated_step(state, y, gates, inplace=True))
+            seq = torch.empty(2, S, C, device="cuda")
+            h, last = after(*W.gated_forward(y.view(1, S, C), x.view(1, S, C), state[:1], out=seq[:1]))
+            dx, dz, dh = after(*W.gated_backward(y.view(1, S, C), x.view(1, S, C), h, state[:1], last))
+            x, dw = after(*W.rms_norm_backward(dx.view(S, C), h.view(S, C), w, dz.view(S, C)))
+            q, scale, _ = after(*W.rms_norm_quant(x, w))
+            kept += [x, dw, q.float(), scale, dh, state.clone()]
+        torch.cuda.synchronize()
+        return kept
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
