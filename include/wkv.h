@@ -381,7 +381,8 @@ WKV_API wkv_status wkv_v6_forward(int64_t B, int64_t T, int64_t H, int64_t D,
  * where z gives the gate:
  *     WKV_GATE_SIGMOID  f = sigmoid(z), i = 1 - f. z = -inf makes f = 0: the
  *                       token starts a sequence of its own (packed rows);
- *                       z = +inf keeps the state.
+ *                       z = +inf keeps the state (padding; its gradients are
+ *                       zero to 2^-126 of the others).
  *     WKV_GATE_DECAY    f = e^{-z}, i = 1 (z as wkv_ext's w_t; z = +inf
  *                       starts a sequence). z < 0 lets the state grow; in
  *                       contract while the product of f over any

@@ -13,7 +13,9 @@ U = 2^-23 (twice the unit roundoff), per token:
     exponential (2 units), the reciprocal (1), the sum and the product before
     them add less than 8 U. The smaller of f and 1 - f carries that relative
     error; so the token's input i|x| and the state's change min(f, 1 - f) A do;
-  * both errors are then carried on by f like the state itself.
+  * both errors are then carried on by f like the state itself;
+  * in gradients 1 - f is held as no less than 2^-126 (a gate of f = 1 is kept
+    as that), so dx may be off by 2^-126 |D| and dz by 2^-126 |D| |h - x|.
 A scan regroups the same sums (its span products carry the same relative
 errors as the factors, and it adds fewer roundings than there are tokens):
 the bound is doubled for it.
@@ -23,6 +25,7 @@ from __future__ import annotations
 import numpy as np
 
 U = 2.0 ** -23
+HELD = 2.0 ** -126
 
 
 def gates(z, gate):
@@ -64,7 +67,7 @@ def allowed_forward(x, z, h0, gate):
     for t in range(x.shape[1]):
         add = i[:, t] * x[:, t]
         new = f[:, t] * A + add
-        E = f[:, t] * E + 4 * U * new + rel[:, t] * (add + low[:, t] * A)
+        E = f[:, t] * E + 4 * U * new + rel[:, t] * low[:, t] * ((x[:, t] if gate == "sigmoid" else 0) + A)
         A = new
         out[:, t], mag[:, t] = 2 * E, A
     return out, mag
@@ -103,10 +106,10 @@ def allowed_backward(x, z, h0, g, dstate, gate):
     for t in range(ax.shape[1] - 1, -1, -1):
         D = ag[:, t] + q
         ED = E + U * D
-        dx[:, t] = 2 * i[:, t] * ED + (rel[:, t] + U) * i[:, t] * D
+        dx[:, t] = 2 * i[:, t] * ED + (rel[:, t] * low[:, t] + 2 * U * i[:, t] + HELD) * D
         w = f[:, t] * i[:, t]
         span = ab[:, t] + (ax[:, t] if gate == "sigmoid" else 0)
-        dz[:, t] = 2 * ED * span * w + D * eb[:, t] * w + D * span * w * (2 * rel[:, t] + 6 * U)
+        dz[:, t] = 2 * ED * span * w + D * eb[:, t] * w + D * span * (w * (2 * rel[:, t] + 6 * U) + HELD)
         E = f[:, t] * ED + 3 * U * f[:, t] * D + rel[:, t] * low[:, t] * D
         q = f[:, t] * D
     return dx, dz, 2 * E

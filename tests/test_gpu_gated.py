@@ -460,3 +460,53 @@ def test_a_wait_that_runs_out_is_reported():
     out, state = W.gated_forward(x, x, workspace=ws)  # the header is ready for the next call
     assert W.query_status(ws) == 0
     check_forward(x, x, None, "sigmoid", out, state)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_masks_of_the_types_extremes(dt):
+    """finfo.min in a sigmoid gate (finfo.max in a decay) starts a sequence, the other end of a sigmoid gate keeps it:
+    e^{+-3e38} is 0 or infinity in any precision."""
+    for T in (40, 300):
+        x, z, h0 = draw(2, T, 34, dt, dt, "sigmoid")
+        z[:, T // 2] = torch.finfo(dt).min
+        z[:, T // 3] = torch.finfo(dt).max
+        out, state = W.gated_forward(x, z, h0)
+        check_forward(x, z, h0, "sigmoid", out, state)
+        assert torch.equal(out[:, T // 2], x[:, T // 2])
+        g = torch.randn(2, T, 34, device="cuda").to(dt)
+        check_backward(x, z, h0, g, None, "sigmoid", W.gated_backward(x, z, g, h0))
+        xd, zd, h0 = draw(2, T, 34, dt, dt, "decay")
+        zd[:, T // 2] = torch.finfo(dt).max
+        zd[:, T // 3] = 0
+        out, state = W.gated_forward(xd, zd, h0, gate="decay")
+        check_forward(xd, zd, h0, "decay", out, state)
+        assert torch.equal(out[:, T // 2], xd[:, T // 2])
+        check_backward(xd, zd, h0, g, None, "decay", W.gated_backward(xd, zd, g, h0, gate="decay"))
+
+
+def test_calls_from_two_host_threads():
+    """Two threads, a stream each, at once: each has a workspace of its own."""
+    import threading
+    jobs = [draw(2, 3000, 128, F32, F32, "sigmoid", seed=i) for i in range(2)]
+    want = [W.gated_forward(*j) for j in jobs]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got[i].append(W.gated_forward(*jobs[i]))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for i in range(2):
+        for out, state in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(state, want[i][1])

@@ -59,9 +59,10 @@ enum { kGateSigmoid = 0, kGateDecay = 1 };
 //     f h + b = A h + (c h + b),
 // which rounds the large h of a slow gate once and holds a small f relative to
 // itself (a state or gradient behind it may be large). A gate of f = 1 is kept
-// as c = -1e-30, so that A is one saturated product and h stays what it is.
-constexpr float kGateHeld = -1e-30f;
-__device__ __forceinline__ float gate_base(float c) { return __saturatef(c * -1e38f); }
+// as c = -2^-126, the smallest normal number, so that A is one saturated
+// product and h stays what it is.
+constexpr float kGateHeld = -1.17549435e-38f;
+__device__ __forceinline__ float gate_base(float c) { return __saturatef(c * -3e38f); }
 __device__ __forceinline__ float2 gate_base(float2 c) { return make_float2(gate_base(c.x), gate_base(c.y)); }
 
 template <int GATE>
