@@ -471,9 +471,9 @@ WKV_API wkv_status wkv_gated_step(int64_t S, int64_t C,
  *   y, sum      contiguous [N, C]; sum takes s in r_dtype and may be residual
  *               where that is contiguous
  *   eps         positive;  groups  1..8192, dividing C
- * Sums are fp32; results are bitwise reproducible. One launch. 16-byte aligned
- * rows with C / groups a multiple of 8 take the fast kernels; any other
- * alignment and size a slower one. N < 2^31, C < 2^24.
+ * Sums are fp32; results are bitwise reproducible. One launch. Rows of 16-byte
+ * alignment with C / groups a multiple of 8 move in 16-byte accesses, others
+ * element by element. N < 2^31, C < 2^24.
  */
 WKV_API wkv_status wkv_rms_norm(int64_t N, int64_t C, int64_t groups, float eps,
                         const void *x, wkv_dtype x_dtype, int64_t x_stride,

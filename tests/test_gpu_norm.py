@@ -51,7 +51,7 @@ def check_sum(s, x, res):
 
 SIZES = [(1, 1, 1), (3, 8, 1), (5, 64, 1), (2, 96, 1), (7, 100, 1), (4, 256, 2), (3, 768, 12), (9, 768, 8), (2, 1024, 1),
          (3, 1032, 1), (2, 4096, 1), (2, 4097, 1), (1, 16384, 1), (1, 20000, 1), (2, 40000, 1), (3, 60, 3), (2, 51, 17),
-         (2, 2048, 2), (5, 3200, 5), (1, 33000, 1)]
+         (2, 2048, 2), (5, 3200, 5), (1, 33000, 1), (65, 57, 1), (33, 250, 10), (9, 771, 1), (40, 1000, 8), (5, 201, 1)]
 
 
 @pytest.mark.parametrize("N,C,groups", SIZES)

@@ -48,15 +48,15 @@ Team cta_team(int64_t n8, int K, bool sc) { return Team{0, K, (int)round_up((siz
 Team fwd_team(int64_t D, bool vec) {
   const int64_t n8 = (D + 7) / 8;
   if (n8 > 4096) return Team{0, 0, 0, false};
-  if (vec && n8 <= 32) {
+  if (n8 <= 32) {
     // a power of two of lanes, or three vectors on a quarter as many where
     // that leaves none idle (96 columns: 4 lanes x 3 against 12 of 16 lanes)
     int tw = 4;
     while (tw < n8) tw *= 2;
-    if (n8 * 4 == 3ll * tw && tw >= 16) return Team{tw / 4, 3, 256, false};
-    return Team{tw, 1, 256, false};
+    if (vec && n8 * 4 == 3ll * tw && tw >= 16) return Team{tw / 4, 3, 256, false};
+    return Team{tw, 1, 256, !vec};
   }
-  if (vec && n8 <= 128) return Team{32, (int)((n8 + 31) / 32), 256, false};
+  if (n8 <= 128) return Team{32, (int)((n8 + 31) / 32), 256, !vec};
   return cta_team(n8, n8 <= 256 ? 1 : n8 <= 1024 ? 2 : n8 <= 2048 ? 4 : 8, !vec);
 }
 
@@ -67,12 +67,12 @@ Team fwd_team(int64_t D, bool vec) {
 // fp32 without gs does better with one (32768 x 4096, gy bf16: 209 and 259).
 Team bwd_team(int64_t D, int64_t G, bool vec, bool s_bf, bool gs) {
   const int64_t n8 = (D + 7) / 8;
-  if (vec && n8 <= 64) {
+  if (n8 <= (vec ? 64 : 32)) {
     int tw = 4;
     while (tw < n8 && tw < 32) tw *= 2;
-    const bool two = n8 > 32 || (s_bf && n8 > 4);
+    const bool two = vec && (n8 > 32 || (s_bf && n8 > 4));
     if (two && n8 <= 32) tw /= 2;
-    if (tw * G <= 512) return Team{tw, two ? 2 : 1, 0, false};
+    if (tw * G <= 512) return Team{tw, two ? 2 : 1, 0, !vec};
   }
   if (G == 1 && n8 <= 2048) return cta_team(n8, n8 <= (vec && (s_bf || gs) ? 96 : 512) ? 1 : n8 <= 1024 ? 2 : 4, !vec);
   return Team{0, 0, 0, false};
@@ -123,7 +123,14 @@ wkv_status launch_team(const NormParams& p, int threads, cudaStream_t st) {
 template <typename X, typename R, bool RES>
 wkv_status fwd_shape(const NormParams& p, const Team& t, cudaStream_t st) {
   if (t.sc) {
-    switch (t.K) {
+    switch (t.TW * 16 + t.K) {
+      case 4 * 16 + 1: return launch_team<X, R, RES, 4, 1, true>(p, t.threads, st);
+      case 8 * 16 + 1: return launch_team<X, R, RES, 8, 1, true>(p, t.threads, st);
+      case 16 * 16 + 1: return launch_team<X, R, RES, 16, 1, true>(p, t.threads, st);
+      case 32 * 16 + 1: return launch_team<X, R, RES, 32, 1, true>(p, t.threads, st);
+      case 32 * 16 + 2: return launch_team<X, R, RES, 32, 2, true>(p, t.threads, st);
+      case 32 * 16 + 3: return launch_team<X, R, RES, 32, 3, true>(p, t.threads, st);
+      case 32 * 16 + 4: return launch_team<X, R, RES, 32, 4, true>(p, t.threads, st);
       case 1: return launch_team<X, R, RES, 0, 1, true>(p, t.threads, st);
       case 2: return launch_team<X, R, RES, 0, 2, true>(p, t.threads, st);
       case 4: return launch_team<X, R, RES, 0, 4, true>(p, t.threads, st);
@@ -225,8 +232,6 @@ wkv_status norm(int64_t N, int64_t C, int64_t G, float eps, const void* x, int x
       cross = vec ? cross_lanes(D, G) : 0;
     }
   }
-  // narrow groups of rows that are not aligned: a CTA each is a waste
-  if (t.sc && t.threads < 64 && G > 1) t.K = 0;
   if ((t.K || cross) && N * G < (1ll << 31)) {
     if (!res)
       return x_dtype == WKV_F32 ? fwd_launch<float, float, false>(p, t, cross, st) : fwd_launch<bf, bf, false>(p, t, cross, st);
@@ -279,7 +284,11 @@ bool bwd_launch(NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
 template <typename Y, typename S, bool GS>
 bool bwd_shape(NormBwdParams& p, const BwdPlan& pl, cudaStream_t st) {
   if (pl.team.sc) {
-    switch (pl.team.K) {
+    switch (pl.team.TW * 8 + pl.team.K) {
+      case 4 * 8 + 1: return bwd_launch<Y, S, GS, 4, 1, true>(p, pl, st);
+      case 8 * 8 + 1: return bwd_launch<Y, S, GS, 8, 1, true>(p, pl, st);
+      case 16 * 8 + 1: return bwd_launch<Y, S, GS, 16, 1, true>(p, pl, st);
+      case 32 * 8 + 1: return bwd_launch<Y, S, GS, 32, 1, true>(p, pl, st);
       case 1: return bwd_launch<Y, S, GS, 0, 1, true>(p, pl, st);
       case 2: return bwd_launch<Y, S, GS, 0, 2, true>(p, pl, st);
       default: return bwd_launch<Y, S, GS, 0, 4, true>(p, pl, st);

@@ -233,7 +233,8 @@ __device__ __forceinline__ float cta_reduce(float v, float* red) {
 // GB/s copy rate): 65536 x 4096 bf16 with residual 311 us (1.06), in e4m3 by
 // 128 columns 274 us (1.05; 461 with one vector and IEEE divisions), e4m3
 // without a residual 166 us (0.74: issue, at 3 bytes a column); 65536 x 12 x 64
-// fp32 60 us (1.02); 40000 x 515 bf16 (SC) 49 us (0.51: 2-byte accesses).
+// fp32 60 us (1.02); rows off 16 bytes: 40000 x 515 bf16 38 us (0.67: 2-byte
+// accesses; 49 with a CTA per row), 65536 x 57 bf16 11 us (0.42; 68).
 template <typename X, typename R, bool RES, int TW, int K, bool SC>
 __global__ void __launch_bounds__(TW ? 256 : 512) wkv_norm_team(const NormParams p) {
   follow_on();
