@@ -385,8 +385,10 @@ WKV_API wkv_status wkv_v6_forward(int64_t B, int64_t T, int64_t H, int64_t D,
  *                       zero to 2^-126 of the others).
  *     WKV_GATE_DECAY    f = e^{-z}, i = 1 (z as wkv_ext's w_t; z = +inf
  *                       starts a sequence). z < 0 lets the state grow; in
- *                       contract while the product of f over any
- *                       WKV_GATED_TILE tokens is finite in fp32.
+ *                       contract while the state, and the product of f over
+ *                       any span of up to WKV_GATED_TILE tokens, are finite
+ *                       in fp32.
+ * What such a span shrinks to less than 2^-126 of itself may be dropped.
  * NaN, and any other infinity, is out of contract. Like the WKV operators it
  * takes whole sequences with the state in and out, single tokens, and has a
  * backward.

@@ -510,3 +510,47 @@ def test_calls_from_two_host_threads():
     for i in range(2):
         for out, state in got[i]:
             assert torch.equal(out, want[i][0]) and torch.equal(state, want[i][1])
+
+
+def growth(kind, T, B, C):
+    """Decays whose product is finite over a tile of 128 tokens (2^92 for z = -1/2) but not over several, on states that
+    stay finite all the same."""
+    g = torch.Generator(device="cuda").manual_seed(C + B)
+    x, z = torch.zeros(B, T, C, device="cuda"), torch.zeros(B, T, C, device="cuda")
+    h0 = torch.zeros(B, C, device="cuda")
+    gr, ds = torch.zeros_like(x), torch.zeros_like(h0)
+    noise = torch.randn(B, T, C, generator=g, device="cuda")
+    if kind == "zero":  # nothing to grow up to the last token (the gradient: down to the first)
+        z.fill_(-0.5)
+        x[:, -1], gr[:, 0] = noise[:, -1], noise[:, 0]
+    elif kind == "small":  # 1e-30 grows by 2^184 in two tiles
+        z[:, 128 * 12:128 * 14] = -0.5
+        h0, ds = 1e-30 * noise[:, 0], 1e-30 * noise[:, 1]
+    elif kind == "start":  # growth of nothing, a start, and ordinary tokens behind it (in front of it for the gradient)
+        z[:, :128 * 11] = -0.5
+        z[:, 128 * 11] = np.inf
+        x[:, 128 * 11:] = noise[:, 128 * 11:]
+        z[:, 128 * 11 + 1:] = 0.01
+        z[:, 128 * 25] = np.inf
+        z[:, 128 * 25 + 1:] = -0.5
+        x[:, 128 * 25:] = 0
+        gr[:, 128 * 11:128 * 25] = noise[:, 128 * 11:128 * 25]
+    else:  # two tiles up, two tiles down, again and again, up at either end
+        z[:, :256 * 19] = torch.where(torch.arange(256 * 19, device="cuda") // 256 % 2 == 0, -0.5, 0.5)[None, :, None]
+        h0, ds = 1e-30 * noise[:, 0], 1e-30 * noise[:, 1]
+    return x, z, h0, gr, ds
+
+
+@pytest.mark.parametrize("kind", ["zero", "small", "start", "waves"])
+@pytest.mark.parametrize("B,C", [(1, 64), (50, 128), (300, 64)])  # look-back groups of 32 tiles, of 8 and of one
+def test_growth_over_many_tiles(B, C, kind):
+    x, z, h0, gr, ds = growth(kind, 128 * 40 + 17, B, C)
+    marks = W.gated_checkpoints(x)
+    out, state = W.gated_forward(x, z, h0, gate="decay", checkpoints=marks)
+    got = W.gated_backward(x, z, gr, h0, ds, gate="decay", checkpoints=marks)
+    for t in (out, state, *got):
+        assert bool(t.isfinite().all())
+    for row in {0, B - 1}:
+        cut = lambda t: t[row:row + 1, ..., C - 9:].contiguous()  # noqa: E731
+        check_forward(cut(x), cut(z), cut(h0), "decay", cut(out), cut(state))
+        check_backward(cut(x), cut(z), cut(h0), cut(gr), cut(ds), "decay", [cut(t) for t in got])

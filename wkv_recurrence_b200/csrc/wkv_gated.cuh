@@ -329,6 +329,33 @@ struct Span {
   float2 P, H;
 };
 __device__ __forceinline__ float2 apply(const Span& s, float2 h) { return fma2(s.P, h, s.H); }
+// Tiles joined: h -> 2^-32 P h + H. A product of several tiles' P may leave
+// fp32's range at either end although each is in it, and so is the state it is
+// applied to. Kept 2^32 times too large it is precise from 2^-158 on; what it
+// loses below would shrink a state of less than 2^32 to nothing in fp32. Larger
+// states, and products that overflow, are found by `peak` and take the tiles
+// one by one.
+constexpr float kLift = 4294967296.f;
+struct Joint {
+  float2 P, H;
+};
+__device__ __forceinline__ float2 apply(const Joint& a, float2 h) {
+  return fma2(mul2(a.P, h), splat(1.f / kLift), a.H);
+}
+__device__ __forceinline__ void join(Joint& a, const Span& s) {
+  a.H = apply(s, a.H);
+  a.P = mul2(a.P, s.P);
+}
+__device__ __forceinline__ void join(Joint& a, const Joint& s) {
+  a.H = apply(s, a.H);
+  a.P = mul2(mul2(a.P, s.P), splat(1.f / kLift));
+}
+// The larger of m and both magnitudes; NaN if one is.
+__device__ __forceinline__ float peak(float m, float2 h) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(h.x)));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(h.y)));
+  return m;
+}
 
 // The state in front of tile `pos` (counted along the scan's direction) comes
 // from the record of the look-back group before it; at pos = 0 it is `first`,
@@ -372,9 +399,21 @@ __device__ __forceinline__ float2 head_get(const GatedParams& p, int item, int p
 // without this, 20 with it).
 template <int NWMAX>
 struct Front {
-  Span part[NWMAX][32];
+  Joint part[NWMAX][32];
   float2 h[32];
 };
+// The state behind the first n tiles of a look-back group (`tot`: its first
+// total) from the state in front of it, tile by tile. All have been waited for.
+__device__ __forceinline__ float2 one_by_one(const GatedRec* tot, int n, uint64_t tag, float2 h) {
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    Span s;
+    rec_load(tot + (size_t)i * kGatedCG, tag, s.P.x, s.H.x);
+    rec_load(tot + (size_t)i * kGatedCG + 1, tag, s.P.y, s.H.y);
+    h = apply(s, h);
+  }
+  return h;
+}
 template <int NWMAX, typename Total>
 __device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, int pos, uint64_t tag, float2 first,
                                               Front<NWMAX>& fr, const Total& own) {
@@ -388,13 +427,13 @@ __device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, in
     rec_put(p, p.tot, ((size_t)item * p.nch + pos) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.nch * kGatedCG, tot.P,
             tot.H, tag);
   }
+  const GatedRec* tots = p.tot + ((size_t)item * p.nch + grp * p.G) * kGatedCG + lane * 2;
   if (w * per < n) {
-    Span a{splat(1.f), splat(0.f)};
+    Joint a{splat(kLift), splat(0.f)};
     for (int i = w * per; i < min(n, (w + 1) * per); ++i) {
       Span s;
-      rec_wait(p.tot + ((size_t)item * p.nch + grp * p.G + i) * kGatedCG + lane * 2, tag, s.P, s.H, p);
-      a.H = apply(s, a.H);
-      a.P = mul2(a.P, s.P);
+      rec_wait(tots + (size_t)i * kGatedCG, tag, s.P, s.H, p);
+      join(a, s);
     }
     fr.part[w][lane] = a;
   }
@@ -407,26 +446,31 @@ __device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, in
   __syncthreads();
   if (hand_on) {
     if (w == 0) {
-      Span a{splat(1.f), splat(0.f)};
+      Joint a{splat(kLift), splat(0.f)};
+      float m = 0.f;
       for (int i = 0; i * per < n; ++i) {
-        const Span s = fr.part[i][lane];
-        a.H = apply(s, a.H);
-        a.P = mul2(a.P, s.P);
+        join(a, fr.part[i][lane]);
+        m = peak(m, a.H);
       }
       const Span tot = own();
-      a.H = apply(tot, a.H);
-      a.P = mul2(tot.P, a.P);
+      join(a, tot);
       float2 P, H = first;
       if (grp > 0) rec_wait(head_rec(p, item, pos), tag, P, H, p);
+      float2 after = apply(a, H);
+      if (!(peak(peak(m, H), after) < kLift)) after = apply(tot, one_by_one(tots, n, tag, H));
       rec_put(p, p.pre, ((size_t)item * p.ngrp + grp) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.ngrp * kGatedCG,
-              splat(0.f), apply(a, H), tag);
+              splat(0.f), after, tag);
       fr.h[lane] = H;
     }
     __syncthreads();
   }
   float2 h = fr.h[lane];
-  for (int i = 0; i * per < n; ++i) h = apply(fr.part[i][lane], h);
-  return h;
+  float m = peak(0.f, h);
+  for (int i = 0; i * per < n; ++i) {
+    h = apply(fr.part[i][lane], h);
+    m = peak(m, h);
+  }
+  return m < kLift ? h : one_by_one(tots, n, tag, fr.h[lane]);
 }
 
 // The tiles of a CTA. Several tiles per sequence: by tickets, so that every
