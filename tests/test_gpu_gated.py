@@ -554,3 +554,35 @@ def test_growth_over_many_tiles(B, C, kind):
         cut = lambda t: t[row:row + 1, ..., C - 9:].contiguous()  # noqa: E731
         check_forward(cut(x), cut(z), cut(h0), "decay", cut(out), cut(state))
         check_backward(cut(x), cut(z), cut(h0), cut(gr), cut(ds), "decay", [cut(t) for t in got])
+
+
+def test_autograd_sees_what_was_written_in_place():
+    """A backward whose saved tensor was overwritten raises, as behind torch's own in-place operators, instead of using
+    what lies there now."""
+    B, T, C = 2, 5, 16
+    x, z, h0 = draw(B, T, C, F32, F32, "sigmoid")
+    x.requires_grad_()
+    other, marks = torch.randn_like(h0), W.gated_checkpoints(x)
+    for overwrite in (lambda: W.gated_step(h0, x[:, 0], z[:, 0], inplace=True),
+                      lambda: W.gated_step(other, x[:, 0], z[:, 0], state_out=h0),
+                      lambda: W.gated_step(other, x[:, 0], z[:, 0], out=h0),
+                      lambda: W.gated_forward(x, z, h0, state_out=h0),
+                      lambda: W.gated_forward(x, z, h0, state_out=h0.view(1, B * C).view(B, C)),
+                      lambda: W.gated_forward(x.detach(), z, out=z)):
+        out, state = W.Gated.apply(x, z, h0, "sigmoid")
+        overwrite()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            (out.sum() + state.sum()).backward()
+    W.Gated.apply(x, z, h0, "sigmoid")[0].sum().backward()  # and nothing else counts as written
+    v = [t._version for t in (x, z, h0, marks)]
+    out, state = W.gated_forward(x, z, h0, checkpoints=marks)
+    W.gated_backward(x, z, torch.ones_like(x), h0, h0, checkpoints=marks)
+    W.gated_step(h0, x[:, 0], z[:, 0])
+    assert [t._version for t in (x, z, h0, marks)] == v[:3] + [v[3] + 1]
+    assert out._version == state._version == 0
+    with torch.inference_mode():
+        h = h0.clone()
+        before = h.clone()
+        W.gated_step(h, x[:, 0], z[:, 0], inplace=True)
+    W.gated_step(h, x[:, 0], z[:, 0], inplace=True)
+    assert not torch.equal(h, before)

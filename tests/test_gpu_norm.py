@@ -330,3 +330,21 @@ def test_a_chain_of_calls_is_ordered(S, C):
     for _ in range(3):
         for a, b in zip(run(False), want):
             assert torch.equal(a, b)
+
+
+def test_autograd_sees_what_was_written_in_place():
+    """A backward whose saved s was overwritten raises, as behind torch's own in-place operators."""
+    x, res, w = draw(6, 64, F32, F32)
+    x.requires_grad_()
+    for overwrite in (lambda s: W.rms_norm(x, w, s, residual_out=s), lambda s: W.rms_norm(x, w, out=s),
+                      lambda s: W.rms_norm_quant(x, w, s, residual_out=s)):
+        y, s = W.RMSNorm.apply(x, w, res)
+        with torch.no_grad():
+            overwrite(s)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+    v = [t._version for t in (x, res, w)]
+    y, s = W.rms_norm(x, w, res)
+    W.rms_norm_quant(x, w, res)
+    W.rms_norm_backward(y, s, w, s)
+    assert [t._version for t in (x, res, w, y, s)] == v + [0, 0]

@@ -128,6 +128,12 @@ void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 Tensor optional(PyObject* o, const char* name, c10::Device dev, at::IntArrayRef shape, ScalarType type) {
   return o == Py_None ? Tensor() : exact(o, name, dev, shape, type);
 }
+// Tells autograd that a tensor of the caller's was written (which torch's own
+// in-place operators do): a backward that saved it before raises. Inference
+// tensors have no version.
+void written(PyObject* given, const Tensor& t) {
+  if (given != Py_None && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 // The output's type: asked for, or that of `out`, or the input's.
 ScalarType out_type(PyObject* dtype, PyObject* out, const Tensor& x, wkv_dtype* code) {
   ScalarType t = x.scalar_type();
@@ -265,6 +271,9 @@ PyObject* gated_forward(PyObject* const* a) {
                              g.z.stride(0), g.z.stride(1), g.gate, out.data_ptr(), ot, (const float*)ptr(state),
                              (float*)state_out.data_ptr(), (float*)ptr(marks), ptr(ws), bytes_of(ws), st);
   });
+  written(a[5], out);
+  written(a[6], state_out);
+  written(a[7], marks);
   return tuple_of({out, state_out});
 }
 
@@ -306,11 +315,14 @@ PyObject* gated_step(PyObject* const* a) {
   const ScalarType os = out_type(a[4], a[5], g.x, &ot);
   const Tensor& state = exact(a[0], "state", g.dev, {S, C}, at::kFloat);
   const Tensor out = result(a[5], "out", g.dev, {S, C}, os);
-  const Tensor state_out = truth(a[7]) ? state : result(a[6], "state_out", g.dev, {S, C}, at::kFloat);
+  PyObject* const to = truth(a[7]) ? a[0] : a[6];
+  const Tensor state_out = result(to, "state_out", g.dev, {S, C}, at::kFloat);
   on_stream(g.dev, "wkv_gated_step", [&](void* st) {
     return lib.gated_step(S, C, g.x.data_ptr(), g.xt, g.x.stride(0), g.z.data_ptr(), g.zt, g.z.stride(0), g.gate,
                           out.data_ptr(), ot, (const float*)state.data_ptr(), (float*)state_out.data_ptr(), st);
   });
+  written(a[5], out);
+  written(to, state_out);
   return tuple_of({out, state_out});
 }
 
@@ -395,6 +407,8 @@ PyObject* rms_norm(PyObject* const* a) {
     return lib.rms_norm(n.N, n.C, n.groups, n.eps, n.x.data_ptr(), n.xt, n.xs, ptr(n.residual), n.rt, n.rs,
                         (const float*)n.weight.data_ptr(), y.data_ptr(), yt, ptr(s), st);
   });
+  written(a[6], y);
+  written(a[7], s);
   return tuple_of({y, s});
 }
 
@@ -414,6 +428,7 @@ PyObject* rms_norm_quant(PyObject* const* a) {
                               (const float*)n.weight.data_ptr(), q.data_ptr(), (float*)scale.data_ptr(), block, ptr(s),
                               st);
   });
+  written(a[6], s);
   return tuple_of({q, scale, s});
 }
 
