@@ -116,3 +116,9 @@ def test_oracle_bound_holds_for_an_fp32_evaluation_and_catches_a_wrong_gate(gate
             h = f[:, t] * h + i[:, t] * x[:, t]
             worst = max(worst, float(((np.abs(h - ref[:, t]) - np.abs(ref[:, t]) * 2.0 ** -24) / al[:, t]).max()))
         assert worst < 1 if off == 0 else worst > 1
+
+
+def test_gated_status_is_offered():
+    assert "gated_status" in W.__all__
+    with pytest.raises((ValueError, RuntimeError)):
+        W.gated_status("cpu")

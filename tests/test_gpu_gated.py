@@ -586,3 +586,28 @@ def test_autograd_sees_what_was_written_in_place():
         W.gated_step(h, x[:, 0], z[:, 0], inplace=True)
     W.gated_step(h, x[:, 0], z[:, 0], inplace=True)
     assert not torch.equal(h, before)
+
+
+def test_a_wait_that_runs_out_on_the_kept_workspace_is_reported():
+    """The same where the caller passes no workspace: the status of the one that is kept for the stream can be queried, and
+    is carried on when a larger one takes its place."""
+    from wkv_recurrence_b200._native import ext
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert W.gated_status() == 0  # none is kept yet
+        x = torch.randn(1, 260, 64, device="cuda")
+        W.gated_forward(x, x)
+        assert W.gated_status() == 0
+        small = ext().gated_kept_workspace(torch.cuda.current_device())
+        assert small.numel() >= W.gated_workspace_size(1, 260, 64)
+        for grow in (False, True):
+            small[:4].view(torch.int32).fill_(1)  # the ticket of tile 0 is gone: its total never arrives
+            W.gated_forward(x, x)
+            if grow:
+                tiles = small.numel() // (8 * 64 * 16) + 1  # 16 bytes for each of 64 channels of 8 groups, and more
+                W.gated_forward(*[torch.zeros(2, 128 * tiles, 256, device="cuda")] * 2)
+                assert ext().gated_kept_workspace(torch.cuda.current_device()).numel() > small.numel()
+            assert W.gated_status(torch.cuda.current_device()) == 6  # WKV_ERR_WAIT_TIMEOUT
+            assert W.gated_status("cuda") == 0
+        out, state = W.gated_forward(x, x)
+        assert W.gated_status() == 0
+        check_forward(x, x, None, "sigmoid", out, state)

@@ -22,10 +22,11 @@ from .api import (WKV, PreparedForward, PreparedStep, WkvError, backward, empty_
                   forward_host, forward_host_buffer_size, forward_kernel, forward_launches, make_workspace,
                   query_status, step, v6_forward, workspace_size)
 from .gated import (Gated, gated_backward, gated_checkpoints, gated_forward, gated_step,  # noqa: F401
-                    gated_workspace_size)
+                    gated_status, gated_workspace_size)
 from .norm import RMSNorm, rms_norm, rms_norm_backward, rms_norm_quant  # noqa: F401
 
 __all__ = ["forward", "forward_host", "forward_host_buffer_size", "step", "backward", "WKV", "v6_forward",
            "workspace_size", "forward_kernel", "forward_launches", "make_workspace", "query_status", "empty_state",
            "PreparedForward", "PreparedStep", "WkvError", "gated_forward", "gated_backward", "gated_step",
-           "gated_checkpoints", "gated_workspace_size", "Gated", "rms_norm", "rms_norm_quant", "rms_norm_backward", "RMSNorm"]
+           "gated_checkpoints", "gated_workspace_size", "gated_status", "Gated", "rms_norm", "rms_norm_quant",
+           "rms_norm_backward", "RMSNorm"]

@@ -199,22 +199,52 @@ Gated gated_inputs(PyObject* ox, PyObject* oz, PyObject* ogate, int64_t dims, co
   return Gated{x, z, xt, zt, gate, x.device()};
 }
 
-// The zero-filled workspace of this device and stream. A call that is being
-// captured gets one of its own, from the graph's memory: graphs captured on
-// one stream may be replayed on several at once.
+// The zero-filled workspaces that are kept, by device and stream.
+struct Kept {
+  std::mutex mu;
+  std::map<std::pair<int, void*>, Tensor> by_stream;
+};
+Kept& kept() {
+  static Kept* k = new Kept;  // never freed: the runtime may be gone at exit
+  return *k;
+}
+std::pair<int, void*> kept_key(c10::Device dev) {
+  return {dev.index(), c10::cuda::getCurrentCUDAStream(dev.index()).stream()};
+}
+
+// The workspace of this device and stream. A call that is being captured gets
+// one of its own, from the graph's memory: graphs captured on one stream may be
+// replayed on several at once.
 Tensor gated_workspace(c10::Device dev, int64_t bytes) {
-  static std::mutex mu;
-  static auto* kept = new std::map<std::pair<int, void*>, Tensor>;  // never freed: the runtime may be gone at exit
   c10::cuda::OptionalCUDAGuard guard;
   if (c10::cuda::current_device() != dev.index()) guard.set_device(dev);
   const auto options = at::TensorOptions().device(dev).dtype(at::kByte);
   if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
     return at::zeros({bytes}, options);
-  void* st = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  std::lock_guard<std::mutex> lk(mu);
-  Tensor& t = (*kept)[{dev.index(), st}];
-  if (!t.defined() || t.numel() < bytes) t = at::zeros({std::max<int64_t>(bytes, 1 << 20)}, options);
+  Kept& k = kept();
+  std::lock_guard<std::mutex> lk(k.mu);
+  Tensor& t = k.by_stream[kept_key(dev)];
+  if (!t.defined() || t.numel() < bytes) {
+    const Tensor more = at::zeros({std::max<int64_t>(bytes, 1 << 20)}, options);
+    if (t.defined()) {  // the status is carried on: a workspace of one tile is its header
+      const int64_t header = (int64_t)lib.gated_workspace_size(1, 1, 1);
+      more.narrow(0, 0, header).copy_(t.narrow(0, 0, header));
+    }
+    t = more;
+  }
   return t;
+}
+
+// (device index): the workspace kept for that device's current stream, or None
+PyObject* gated_kept_workspace(PyObject* const* a) {
+  Tensor t;
+  {
+    Kept& k = kept();
+    std::lock_guard<std::mutex> lk(k.mu);
+    const auto at = k.by_stream.find(kept_key(c10::Device(c10::kCUDA, (c10::DeviceIndex)integer(a[0]))));
+    if (at != k.by_stream.end()) t = at->second;
+  }
+  return t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
 }
 
 Tensor gated_scratch(PyObject* o, int64_t B, int64_t T, int64_t C, c10::Device dev) {
@@ -530,6 +560,7 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&bind)), METH_FASTCALL, nullptr},
+    WKV_ENTRY(gated_kept_workspace, 1),
     WKV_ENTRY(gated_checkpoints, 1),
     WKV_ENTRY(gated_forward, 9),
     WKV_ENTRY(gated_backward, 8),

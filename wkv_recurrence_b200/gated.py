@@ -18,6 +18,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _abi
 from ._native import ext
+from .api import query_status
 
 
 def gated_workspace_size(B: int, T: int, C: int) -> int:
@@ -26,6 +27,18 @@ def gated_workspace_size(B: int, T: int, C: int) -> int:
     if n == 0:
         raise ValueError("invalid sizes")
     return int(n)
+
+
+def gated_status(device=None) -> int:
+    """Synchronise the current stream of ``device`` (default: the current one)
+    and return and clear the status of the workspace that is kept for it: 0, or 6
+    (WKV_ERR_WAIT_TIMEOUT) if a wait inside a ``gated_forward``,
+    ``gated_backward`` or ``Gated`` on that stream, without a workspace of the
+    caller's, gave up since the last query. The results of such a call are not
+    valid. ``query_status`` is the same for a caller's workspace."""
+    with torch.cuda.device(torch.cuda.current_device() if device is None else torch.device(device)):
+        kept = ext().gated_kept_workspace(torch.cuda.current_device())
+        return 0 if kept is None else query_status(kept)
 
 
 def gated_checkpoints(x: torch.Tensor) -> torch.Tensor:
@@ -46,8 +59,9 @@ def gated_forward(x: torch.Tensor, z: torch.Tensor, state: Optional[torch.Tensor
     Returns (out [B, T, C], state after the last token). state_out may be
     ``state``. checkpoints: a ``gated_checkpoints(x)`` tensor to be filled for
     ``gated_backward``. workspace: ``gated_workspace_size`` bytes, zero-filled
-    once, for this operator alone; by default one is kept per stream (and
-    allocated anew in a call that is captured into a graph).
+    once, for this operator alone; by default one is kept per stream (see
+    ``gated_status``). A call that is captured into a graph gets one in the
+    graph's memory, whose status cannot be queried: pass one where it matters.
     """
     return ext().gated_forward(x, z, state, gate, out_dtype, out, state_out, checkpoints, workspace)
 
