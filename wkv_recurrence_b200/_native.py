@@ -1,6 +1,7 @@
 """Loads _wkv_torch.so, the native calling path of the gated recurrence and the
 RMS norm (csrc/wkv_torch.cpp), and binds it to the library that _abi loaded.
-Fails loudly if it has not been built; there is no other path.
+Fails loudly if it has not been built, or was built against another torch or
+interpreter; there is no other path.
 """
 from __future__ import annotations
 
@@ -27,6 +28,10 @@ def ext():
         spec = importlib.util.spec_from_file_location("_wkv_torch", PATH)
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
+        from . import build
+        if mod.built_for() != build.ext_key():
+            raise RuntimeError(f"_wkv_torch.so is built for {mod.built_for()}, and this is {build.ext_key()}; "
+                               "run python -m wkv_recurrence_b200.build")
         mod.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES}, _abi.check,
                  torch.OutOfMemoryError)
         _ext = mod

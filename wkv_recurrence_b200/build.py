@@ -65,9 +65,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     return out
 
 
+def ext_key() -> str:
+    """What _wkv_torch.so is compiled against besides its sources: torch, its C++
+    ABI and the interpreter. An object built for another key is not loaded."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, C++11 ABI {int(torch.compiled_with_cxx11_abi())}, {sysconfig.get_config_var('SOABI')}"
+
+
 def build_ext(force: bool = False, verbose: bool = False) -> str:
-    """_wkv_torch.so: host code against the installed torch's headers."""
-    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(p) for p in (TORCH, HEADER)):
+    """_wkv_torch.so: host code against the installed torch's headers. Its key is
+    in the object, and beside it for this check."""
+    key, stamp = ext_key(), EXT + ".key"
+    if (not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(p) for p in (TORCH, HEADER))
+            and os.path.exists(stamp) and open(stamp).read() == key):
         return EXT
     import sysconfig
 
@@ -77,7 +89,7 @@ def build_ext(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(os.path.dirname(EXT), exist_ok=True)
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f'-DWKV_EXT_KEY="{key}"',
            f"-I{base}/include", f"-I{base}/include/torch/csrc/api/include", f"-I{cuda}/include",
            f"-I{sysconfig.get_paths()['include']}", "-o", tmp, TORCH,
            f"-L{base}/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
@@ -85,6 +97,8 @@ def build_ext(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, EXT)
+    with open(stamp, "w") as f:
+        f.write(key)
     return EXT
 
 

@@ -555,11 +555,15 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// what the object was compiled against (build.py: ext_key)
+PyObject* built_for(PyObject*, PyObject*) { return PyUnicode_FromString(WKV_EXT_KEY); }
+
 #define WKV_ENTRY(name, n) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<name, n>)), METH_FASTCALL, nullptr}
 
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&bind)), METH_FASTCALL, nullptr},
+    {"built_for", &built_for, METH_NOARGS, nullptr},
     WKV_ENTRY(gated_kept_workspace, 1),
     WKV_ENTRY(gated_checkpoints, 1),
     WKV_ENTRY(gated_forward, 9),
