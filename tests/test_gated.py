@@ -122,3 +122,18 @@ def test_gated_status_is_offered():
     assert "gated_status" in W.__all__
     with pytest.raises((ValueError, RuntimeError)):
         W.gated_status("cpu")
+
+
+def test_states_off_four_bytes_are_refused(L):
+    """A state, checkpoint or gradient pointer that no float can be read from."""
+    n = L.wkv_gated_workspace_size(1, 129, 4)
+    for at in range(3):
+        ptr = [None, None, P(256)]
+        ptr[at] = P(258)
+        assert L.wkv_gated_forward(1, 129, 4, P(256), F32, 516, 4, P(256), F32, 516, 4, 0, P(256), F32, *ptr, P(256), n - 1,
+                                   None) == _abi.WKV_ERR_MISALIGNED
+    for at in (0, 1, 2, 5):
+        ptr = [None, None, P(256), P(256), P(256), None]  # state, dstate, checkpoints, dx, dz, dstate_in
+        ptr[at] = P(257)
+        assert L.wkv_gated_backward(1, 129, 4, P(256), F32, 516, 4, P(256), F32, 516, 4, 0, P(256), F32, *ptr, P(256), n - 1,
+                                    None) == _abi.WKV_ERR_MISALIGNED

@@ -236,6 +236,7 @@ wkv_status wkv_gated_forward(int64_t B, int64_t T, int64_t C, const void* x, wkv
                                       z_token_stride, gate, out_dtype);
   if (chk != WKV_OK) return chk;
   if (out && !aligned(out, elem(out_dtype))) return WKV_ERR_MISALIGNED;
+  if (!aligned(state_in, 4) || !aligned(state_out, 4) || !aligned(checkpoints, 4)) return WKV_ERR_MISALIGNED;
   GatedPlan pl;
   if (!gated_plan(B, T, C, &pl)) return WKV_ERR_INVALID_ARG;
   const wkv_status wchk = check_workspace(pl, workspace, workspace_bytes);
@@ -276,6 +277,8 @@ wkv_status wkv_gated_backward(int64_t B, int64_t T, int64_t C, const void* x, wk
   const bool any = B > 0 && T > 0 && C > 0;
   if (any && (!gout || !dx || !dz)) return WKV_ERR_INVALID_ARG;
   if (any && (!aligned(gout, elem(g_dtype)) || !aligned(dx, elem(x_dtype)) || !aligned(dz, elem(z_dtype))))
+    return WKV_ERR_MISALIGNED;
+  if (!aligned(state_in, 4) || !aligned(dstate_out, 4) || !aligned(checkpoints, 4) || !aligned(dstate_in, 4))
     return WKV_ERR_MISALIGNED;
   GatedPlan pl;
   if (!gated_plan(B, T, C, &pl)) return WKV_ERR_INVALID_ARG;
