@@ -611,3 +611,22 @@ def test_a_wait_that_runs_out_on_the_kept_workspace_is_reported():
         out, state = W.gated_forward(x, x)
         assert W.gated_status() == 0
         check_forward(x, x, None, "sigmoid", out, state)
+
+
+def test_a_call_under_a_torch_mode_leaves_no_trace():
+    """A call that is refused because its tensors hold no data, and a call under a mode that replaces what torch's operators
+    return, do not spoil the workspace kept for the calls after them."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    x, z, h0 = draw(2, 300, 64, F32, F32, "sigmoid")
+    want = W.gated_forward(x, z, h0)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with FakeTensorMode() as mode:
+            fake = mode.from_tensor(x)
+            with pytest.raises(RuntimeError):
+                W.gated_forward(fake, fake)
+            inside = W.gated_forward(x, z, h0)
+        after = W.gated_forward(x, z, h0)
+        torch.cuda.current_stream().synchronize()
+    for got in (inside, after):
+        assert type(got[0]) is torch.Tensor and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -11,6 +11,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -212,24 +213,30 @@ std::pair<int, void*> kept_key(c10::Device dev) {
   return {dev.index(), c10::cuda::getCurrentCUDAStream(dev.index()).stream()};
 }
 
+// Zero bytes, by no operator of torch's: under its modes and transforms these
+// may return other than plain tensors, and a workspace is kept for later calls.
+Tensor zeros(c10::Device dev, int64_t bytes, cudaStream_t st) {
+  const Tensor t = fresh(dev, {bytes}, at::kByte);
+  C10_CUDA_CHECK(cudaMemsetAsync(t.data_ptr(), 0, (size_t)bytes, st));
+  return t;
+}
+
 // The workspace of this device and stream. A call that is being captured gets
 // one of its own, from the graph's memory: graphs captured on one stream may be
 // replayed on several at once.
 Tensor gated_workspace(c10::Device dev, int64_t bytes) {
   c10::cuda::OptionalCUDAGuard guard;
   if (c10::cuda::current_device() != dev.index()) guard.set_device(dev);
-  const auto options = at::TensorOptions().device(dev).dtype(at::kByte);
-  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
-    return at::zeros({bytes}, options);
+  cudaStream_t st = c10::cuda::getCurrentCUDAStream(dev.index());
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return zeros(dev, bytes, st);
   Kept& k = kept();
   std::lock_guard<std::mutex> lk(k.mu);
-  Tensor& t = k.by_stream[kept_key(dev)];
+  Tensor& t = k.by_stream[{dev.index(), st}];
   if (!t.defined() || t.numel() < bytes) {
-    const Tensor more = at::zeros({std::max<int64_t>(bytes, 1 << 20)}, options);
-    if (t.defined()) {  // the status is carried on: a workspace of one tile is its header
-      const int64_t header = (int64_t)lib.gated_workspace_size(1, 1, 1);
-      more.narrow(0, 0, header).copy_(t.narrow(0, 0, header));
-    }
+    const Tensor more = zeros(dev, std::max<int64_t>(bytes, 1 << 20), st);
+    if (t.defined())  // the status is carried on: a workspace of one tile is its header
+      C10_CUDA_CHECK(cudaMemcpyAsync(more.data_ptr(), t.data_ptr(), lib.gated_workspace_size(1, 1, 1),
+                                     cudaMemcpyDeviceToDevice, st));
     t = more;
   }
   return t;
