@@ -630,3 +630,15 @@ def test_a_call_under_a_torch_mode_leaves_no_trace():
         torch.cuda.current_stream().synchronize()
     for got in (inside, after):
         assert type(got[0]) is torch.Tensor and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_step_in_place_takes_no_other_state_out():
+    x, z, h0 = draw(3, 1, 64, F32, F32, "sigmoid")
+    x, z, other = x[:, 0], z[:, 0], torch.zeros_like(h0)
+    with pytest.raises(ValueError, match="inplace"):
+        W.gated_step(h0, x, z, state_out=other, inplace=True)
+    want = W.gated_step(h0, x, z)
+    for inplace in (False, True):
+        s = h0.clone()
+        out, state = W.gated_step(s, x, z, state_out=s, inplace=inplace)
+        assert state is s and torch.equal(state, want[1]) and torch.equal(out, want[0])

@@ -352,7 +352,9 @@ PyObject* gated_step(PyObject* const* a) {
   const ScalarType os = out_type(a[4], a[5], g.x, &ot);
   const Tensor& state = exact(a[0], "state", g.dev, {S, C}, at::kFloat);
   const Tensor out = result(a[5], "out", g.dev, {S, C}, os);
-  PyObject* const to = truth(a[7]) ? a[0] : a[6];
+  const bool inplace = truth(a[7]);
+  if (inplace && a[6] != Py_None && a[6] != a[0]) bad_value("state_out must be left out (or be state) with inplace");
+  PyObject* const to = inplace ? a[0] : a[6];
   const Tensor state_out = result(to, "state_out", g.dev, {S, C}, at::kFloat);
   on_stream(g.dev, "wkv_gated_step", [&](void* st) {
     return lib.gated_step(S, C, g.x.data_ptr(), g.xt, g.x.stride(0), g.z.data_ptr(), g.zt, g.z.stride(0), g.gate,

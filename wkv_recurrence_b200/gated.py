@@ -85,8 +85,8 @@ def gated_step(state: torch.Tensor, x: torch.Tensor, z: torch.Tensor, *, gate: s
                out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
                state_out: Optional[torch.Tensor] = None, inplace: bool = False):
     """One token for S streams: x, z [S, C] (channel axis contiguous), state
-    float32 [S, C]. Returns (out [S, C], new state); with ``inplace=True`` the
-    state tensor is updated in place and returned."""
+    float32 [S, C]. Returns (out [S, C], new state). With ``inplace=True`` the
+    state tensor is updated in place and returned, as with state_out=state."""
     return ext().gated_step(state, x, z, gate, out_dtype, out, state_out, inplace)
 
 
