@@ -642,3 +642,34 @@ def test_a_step_in_place_takes_no_other_state_out():
         s = h0.clone()
         out, state = W.gated_step(s, x, z, state_out=s, inplace=inplace)
         assert state is s and torch.equal(state, want[1]) and torch.equal(out, want[0])
+
+
+@pytest.mark.parametrize("gate", ["sigmoid", "decay"])
+@pytest.mark.parametrize("xt,zt,ot", TYPES)
+@pytest.mark.parametrize("C", [64, 128, 768])
+@pytest.mark.parametrize("T", [129, 517, 1024])
+def test_whole_tiles_of_every_type(T, C, xt, zt, ot, gate):
+    """Rows of 16-byte copies, channel groups of 64 and spans that are full."""
+    x, z, h0 = draw(2, T, C, xt, zt, gate, seed=3)
+    marks = W.gated_checkpoints(x)
+    out, state = W.gated_forward(x, z, h0, gate=gate, out_dtype=ot, checkpoints=marks)
+    g, ds = torch.randn(2, T, C, device="cuda").to(ot), torch.randn(2, C, device="cuda")
+    got = W.gated_backward(x, z, g, h0, ds, gate=gate, checkpoints=marks)
+    check_forward(x, z, h0, gate, out, state)
+    check_backward(x, z, h0, g, ds, gate, got)
+
+
+@pytest.mark.parametrize("gate", ["sigmoid", "decay"])
+@pytest.mark.parametrize("xt,zt,ot", TYPES)
+def test_many_channel_groups_of_every_type(xt, zt, ot, gate):
+    """256 channel groups and more: every tile takes the state from the one before it (look-back groups of one)."""
+    B, T, C = 33, 400, 512
+    x, z, h0 = draw(B, T, C, xt, zt, gate, seed=4)
+    marks = W.gated_checkpoints(x)
+    out, state = W.gated_forward(x, z, h0, gate=gate, out_dtype=ot, checkpoints=marks)
+    g, ds = torch.randn(B, T, C, device="cuda").to(ot), torch.randn(B, C, device="cuda")
+    got = W.gated_backward(x, z, g, h0, ds, gate=gate, checkpoints=marks)
+    for row, cols in ((0, slice(0, 130)), (17, slice(190, 258)), (B - 1, slice(C - 70, C))):
+        cut = lambda t: t[row:row + 1, ..., cols].contiguous()  # noqa: E731
+        check_forward(cut(x), cut(z), cut(h0), gate, cut(out), cut(state))
+        check_backward(cut(x), cut(z), cut(h0), cut(g), cut(ds), gate, [cut(t) for t in got])
