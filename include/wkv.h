@@ -406,7 +406,10 @@ WKV_API wkv_status wkv_v6_forward(int64_t B, int64_t T, int64_t H, int64_t D,
  *               shape that fits, one call at a time, and is kept apart from
  *               the workspaces of the other operators. Its status word reports
  *               device-side wait timeouts (wkv_query_status).
- * The arithmetic and the state are fp32; 1 - f is carried where f is near 1.
+ * The arithmetic and the state are fp32. For f <= 1 the smaller of f and 1 - f
+ * is carried, f > 1 is a rounded fp32 number. Either way the state is rounded
+ * too: one that is carried on nearly unchanged for n tokens may be off by
+ * n 2^-23 of itself.
  * Results are bitwise reproducible. One launch.
  */
 typedef enum { WKV_GATE_SIGMOID = 0, WKV_GATE_DECAY = 1 } wkv_gate;
@@ -475,7 +478,7 @@ WKV_API wkv_status wkv_gated_step(int64_t S, int64_t C,
  *   eps         positive;  groups  1..8192, dividing C
  * Sums are fp32; results are bitwise reproducible. One launch. Rows of 16-byte
  * alignment with C / groups a multiple of 8 move in 16-byte accesses, others
- * element by element. N < 2^31, C < 2^24.
+ * element by element. N < 2^31, C < 2^24, strides up to 2^31.
  */
 WKV_API wkv_status wkv_rms_norm(int64_t N, int64_t C, int64_t groups, float eps,
                         const void *x, wkv_dtype x_dtype, int64_t x_stride,
@@ -485,8 +488,12 @@ WKV_API wkv_status wkv_rms_norm(int64_t N, int64_t C, int64_t groups, float eps,
 /*
  * wkv_rms_norm with y in 8 bits: q [N, C] in e4m3 (contiguous) and scale
  * [N, C / block] fp32, scale = max |y| / 448 over its block of columns (1 for
- * a block of zeros), q = y / scale rounded to nearest even. block: 32, 64 or
- * 128 and dividing C, or 0 (or C) for one scale per row.
+ * a block of zeros), q = y / scale rounded to e4m3. block: 32, 64 or 128 and
+ * dividing C, or 0 (or C) for one scale per row. The quotient is formed in fp32
+ * as s weight (r / scale) with an approximate reciprocal, so a y / scale within
+ * 2^-20 of itself of the middle between two e4m3 numbers may round to either.
+ * Columns whose y is NaN are NaN in q and left out of the maximum (a block of
+ * nothing else has scale 1).
  */
 WKV_API wkv_status wkv_rms_norm_quant(int64_t N, int64_t C, int64_t groups, float eps,
                               const void *x, wkv_dtype x_dtype, int64_t x_stride,

@@ -348,3 +348,27 @@ def test_autograd_sees_what_was_written_in_place():
     W.rms_norm_quant(x, w, res)
     W.rms_norm_backward(y, s, w, s)
     assert [t._version for t in (x, res, w, y, s)] == v + [0, 0]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("C,groups,block,shift", [(512, 1, 128, 0), (512, 1, 0, 0), (768, 12, 64, 0), (768, 12, 128, 0),
+                                                  (768, 12, 0, 0), (8192, 1, 128, 0), (768, 12, 128, 1), (2560, 5, 128, 0),
+                                                  (100, 1, 0, 0)])
+def test_quant_of_what_is_not_finite(C, groups, block, shift, bad):
+    """A NaN or an infinity makes its group NaN (an infinity: itself alone, the others 0); it is NaN in q, and the scale is
+    that of the block's other columns. Other rows do not notice."""
+    x, _, w = draw(3, C + shift, F32, None)
+    x, w = x[:, shift:], w[shift:].contiguous()
+    x[1, C // groups + 3 if groups > 1 else 3] = bad
+    q, scale, _ = W.rms_norm_quant(x, w, groups=groups, block=block)
+    y, _ = W.rms_norm(x, w, groups=groups)
+    assert bool(y[1].isnan().any()) and torch.equal(q.float().isnan(), y.isnan())
+    b = block or C
+    top = y[1].view(-1, b).nan_to_num(0.0).abs().amax(-1)
+    want = torch.where(top > 0, top / 448, torch.ones_like(top))
+    assert bool(((scale[1] - want).abs() <= want * 2.0 ** -20).all())
+    good = q[1].float().view(-1, b) * scale[1][:, None]
+    err = (good - y[1].view(-1, b)).nan_to_num(0.0).abs()
+    assert bool((err <= top[:, None] * 2.0 ** -4 * 1.001).all())
+    keep = torch.tensor([0, 2], device="cuda")
+    check_q(q[keep], scale[keep], x[keep], w, groups, block)

@@ -154,7 +154,6 @@ wkv_status step_launch(int gate, int V, const GatedStepParams& p, cudaStream_t s
     if (V == 4) return launch_follow_on(gated_step_kernel<X, Z, O, kGateDecay, 4>, grid, 256, 0, st, p);
     else return launch_follow_on(gated_step_kernel<X, Z, O, kGateDecay, 1>, grid, 256, 0, st, p);
   }
-  return launch_result();
 }
 
 // A state passed through unchanged (no tokens): copied, or zeros.

@@ -38,7 +38,9 @@ def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     """``rms_norm`` with its output in 8 bits: (q, scale, s) with q [..., C]
     float8_e4m3fn, scale float32 [..., C / block] and q * scale close to y.
     block: columns per scale: 32, 64 or 128 (dividing C), or 0 for the whole
-    row. scale = max |y| / 448 of its block, 1 for a block of zeros.
+    row. scale = max |y| / 448 of its block, 1 for a block of zeros. q is y / scale
+    rounded to e4m3; next to the middle of two e4m3 numbers either may be taken.
+    Columns whose y is NaN are NaN in q and left out of the maximum.
     """
     return ext().rms_norm_quant(x, weight, residual, eps, groups, block, residual_out)
 
