@@ -29,9 +29,10 @@
 // polls the data itself.
 //
 // Bound: memory traffic (12 bytes per element fp32, 6 bf16; backward 20/10) in
-// fp32, instruction issue in bf16 (55-60% of the slots are filled, 28
-// instructions per element forward and 54 backward); pairs of channels are
-// computed with the two-wide fp32 instructions, which took 14% off.
+// fp32; in bf16, with half the bytes behind the same instructions (28 per
+// element forward and 54 backward), latency: 16 warps per SM fill 55-60% of the
+// issue slots and wait for copies, barriers and their own results. Pairs of
+// channels are computed with the two-wide fp32 instructions, which took 14% off.
 //
 // Tile: 128 tokens by eight warps of 16, two CTAs per SM at 128 registers. What
 // a warp spends on a tile besides its tokens (copies' addresses, joining spans,
@@ -352,8 +353,7 @@ __device__ __forceinline__ void join(Joint& a, const Joint& s) {
 }
 // The larger of m and both magnitudes; NaN if one is.
 __device__ __forceinline__ float peak(float m, float2 h) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(h.x)));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(h.y)));
+  asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(h.x)), "f"(fabsf(h.y)));
   return m;
 }
 
@@ -395,8 +395,8 @@ __device__ __forceinline__ float2 head_get(const GatedParams& p, int item, int p
 // `pos` in its group, which do not wait for the chain, and warp 0 the record.
 // The tile that ends its group is a link of the chain: there warp 0 first joins
 // all totals, its own tile's included, then waits for the record and hands the
-// state on at once, before the other warps know it (1 x 65536 x 64: 70 us
-// without this, 20 with it).
+// state on at once, before the other warps know it (1 x 65536 x 64, inputs in
+// L2: 70 us without this, 20 with it).
 template <int NWMAX>
 struct Front {
   Joint part[NWMAX][32];
@@ -520,9 +520,10 @@ struct GatedShared {
 // forward
 // ---------------------------------------------------------------------------
 // Measured (of the 6521 GB/s copy rate, for each input read and each output
-// written once): 1 x 65536 x 2048 fp32 304 us (0.81), 16 x 4096 x 4096 with
-// bf16 x and out and fp32 decays 343 us (0.96), all bf16 344 us (0.72; issue),
-// 8 x 1024 x 768 bf16 14.3 us (0.41: 2.6 rounds of tiles).
+// written once; inputs from DRAM): 1 x 65536 x 2048 fp32 310 us (0.80; 307
+// with joined tiles' products unscaled), 16 x 4096 x 4096 with bf16 x and out
+// and fp32 decays 344 us (0.96), all bf16 341 us (0.72), 8 x 1024 x 768 bf16
+// 16.8 us (0.35: three rounds of tiles, about 5 us each; 14.3 us out of L2).
 template <typename X, typename Z, int J, int NW>
 constexpr size_t gated_fwd_smem() {
   return (size_t)J * NW * kGatedCG * (sizeof(X) + sizeof(Z));
@@ -648,9 +649,9 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
 // x and z are fetched one tile ahead as soon as the states are done; g has two
 // buffers where both fit beside another CTA (kGB), else it is fetched last.
 //
-// Measured: 1 x 65536 x 2048 fp32 471 us (0.87), 16 x 4096 x 4096 bf16 with
-// fp32 decays 624-660 us (0.87-0.92), all bf16 617 us (0.67; issue), 8 x 1024 x
-// 768 bf16 22.1 us (0.44).
+// Measured: 1 x 65536 x 2048 fp32 488 us (0.84; 478 unscaled), 16 x 4096 x 4096
+// bf16 with fp32 decays 627 us (0.92; 670-720 back to back under the power cap),
+// all bf16 609 us (0.68), 8 x 1024 x 768 bf16 24.1 us (0.40; 22.1 out of L2).
 template <typename X, typename Z, typename O, int J, int NW>
 struct GatedBwdSmem {
   static constexpr size_t kRow = (size_t)J * NW * kGatedCG;
@@ -826,8 +827,8 @@ struct GatedStepParams {
 
 // Elementwise and bound by memory (20 bytes per stream-channel in fp32, 14 in
 // bf16); four channels per thread move as 16-byte accesses of the state. Steps
-// of 4096 x 768 bf16, one after the other: 6.7 us (1.0 of the copy rate; 8.2
-// each waiting for its launch).
+// of 4096 x 768 bf16, one after the other: 6.7 us on the same 44 MB (in L2), 8.4
+// us from DRAM (0.80 of the copy rate).
 template <typename X, typename Z, typename O, int GATE, int V>
 __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepParams p) {
   follow_on();
