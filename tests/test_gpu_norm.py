@@ -372,3 +372,50 @@ def test_quant_of_what_is_not_finite(C, groups, block, shift, bad):
     assert bool((err <= top[:, None] * 2.0 ** -4 * 1.001).all())
     keep = torch.tensor([0, 2], device="cuda")
     check_q(q[keep], scale[keep], x[keep], w, groups, block)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_that_wait_for_another_stream(captured):
+    """A call behind an event of another stream reads what that stream's calls wrote, although it is launched before the
+    call in front of it on its own stream ends; eager, and as the join of two branches of a graph."""
+    N, C = 8192, 2048
+    x, res, w = draw(N, C, F32, F32)
+    gates = torch.randn(N, C, device="cuda")
+    y0, s0 = W.rms_norm(x, w, res)
+    small, _ = W.rms_norm(x[:16].contiguous(), w)
+    want = W.gated_step(s0, y0, gates)
+    wx, wdw = W.rms_norm_backward(want[0], want[1], w)
+    torch.cuda.synchronize()
+    other, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    y, s = torch.zeros_like(x), torch.zeros_like(x)
+    head = torch.zeros_like(small)
+
+    def run():
+        fork, join = torch.cuda.Event(), torch.cuda.Event()
+        fork.record()
+        other.wait_event(fork)
+        with torch.cuda.stream(other):
+            for _ in range(3):
+                W.rms_norm(x, w, res, out=y, residual_out=s)
+            join.record()
+        W.rms_norm(x[:16], w, out=head)
+        torch.cuda.current_stream().wait_event(join)
+        out, state = W.gated_step(s, y, gates)
+        return (out, state, *W.rms_norm_backward(out, state, w))
+
+    with torch.cuda.stream(mine):
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=mine):
+                got = run()
+        for _ in range(10):
+            y.zero_()
+            s.zero_()
+            if captured:
+                graph.replay()
+            else:
+                got = run()
+            mine.synchronize()
+            for a, b in zip(got, (*want, wx, wdw)):
+                assert torch.equal(a, b)
+            assert torch.equal(head, small)

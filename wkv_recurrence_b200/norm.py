@@ -58,7 +58,8 @@ def rms_norm_backward(gy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, g
 class RMSNorm(torch.autograd.Function):
     """``rms_norm`` as a torch autograd function, differentiable in x, weight and
     residual: ``RMSNorm.apply(x, weight, residual, eps, groups)`` returns (y, s),
-    or y alone where residual is None."""
+    or y alone where residual is None. Under graph capture call ``rms_norm`` and
+    ``rms_norm_backward`` themselves."""
 
     @staticmethod
     def forward(ctx, x, weight, residual=None, eps=1e-6, groups=1):
