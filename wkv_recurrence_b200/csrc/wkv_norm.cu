@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -265,7 +266,10 @@ bool resident(F fn, int threads, size_t smem, int* ctas) {
       !cuda_ok(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
     return false;
   *ctas = std::max(1, per) * sms;
-  known.push_back({fn, Entry{dev, threads, *ctas, smem}});
+  try {
+    known.push_back({fn, Entry{dev, threads, *ctas, smem}});
+  } catch (const std::bad_alloc&) {  // no exception leaves a C entry; looked up again next time
+  }
   return true;
 }
 
