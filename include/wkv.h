@@ -388,7 +388,8 @@ WKV_API wkv_status wkv_v6_forward(int64_t B, int64_t T, int64_t H, int64_t D,
  *                       contract while the state, and the product of f over
  *                       any span of up to WKV_GATED_TILE tokens, are finite
  *                       in fp32.
- * What such a span shrinks to less than 2^-126 of itself may be dropped.
+ * What a span of tokens shrinks to less than 2^-126 of itself may be dropped
+ * (behind a decay, which may grow it again, a span of up to WKV_GATED_TILE).
  * NaN, and any other infinity, is out of contract. Like the WKV operators it
  * takes whole sequences with the state in and out, single tokens, and has a
  * backward.

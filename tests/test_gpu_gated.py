@@ -673,3 +673,21 @@ def test_many_channel_groups_of_every_type(xt, zt, ot, gate):
         cut = lambda t: t[row:row + 1, ..., cols].contiguous()  # noqa: E731
         check_forward(cut(x), cut(z), cut(h0), gate, cut(out), cut(state))
         check_backward(cut(x), cut(z), cut(h0), cut(g), cut(ds), gate, [cut(t) for t in got])
+
+
+@pytest.mark.parametrize("gate,starts,slow", [("sigmoid", False, False), ("sigmoid", True, False), ("decay", False, True),
+                                              ("decay", True, False)])
+@pytest.mark.parametrize("size", [1e12, 1e30])
+@pytest.mark.parametrize("B,C", [(1, 64), (50, 40)])
+def test_large_states(B, C, size, gate, starts, slow):
+    """States far above 2^32, fast and slow gates: as small ones, at their scale."""
+    x, z, h0 = draw(B, 128 * 40 + 17, C, F32, F32, gate, seed=6, starts=starts, slow=slow)
+    x, h0 = size * x, size * h0
+    marks = W.gated_checkpoints(x)
+    out, state = W.gated_forward(x, z, h0, gate=gate, checkpoints=marks)
+    g, ds = torch.randn_like(x), torch.randn_like(h0)
+    got = W.gated_backward(x, z, g / size, h0, ds / size, gate=gate, checkpoints=marks)
+    for row in {0, B - 1}:
+        cut = lambda t: t[row:row + 1, ..., C - 9:].contiguous()  # noqa: E731
+        check_forward(cut(x), cut(z), cut(h0), gate, cut(out), cut(state))
+        check_backward(cut(x), cut(z), cut(h0), cut(g / size), cut(ds / size), gate, [cut(t) for t in got])

@@ -332,11 +332,12 @@ struct Span {
 __device__ __forceinline__ float2 apply(const Span& s, float2 h) { return fma2(s.P, h, s.H); }
 // Tiles joined: h -> 2^-32 P h + H. A product of several tiles' P may leave
 // fp32's range at either end although each is in it, and so is the state it is
-// applied to. Kept 2^32 times too large it is precise from 2^-158 on; what it
-// loses below would shrink a state of less than 2^32 to nothing in fp32. Larger
-// states, and products that overflow, are found by `peak` and take the tiles
-// one by one.
-constexpr float kLift = 4294967296.f;
+// applied to. It is kept 2^32 times too large, and as 0 below 2^-158, where it
+// shrinks a state of less than 2^32 to nothing in fp32. Products that overflow,
+// and larger states in front of such a 0 if later gates may be above 1 (GROWS),
+// are found by `peak` and take the tiles one by one (1 x 65536 x 2048 fp32 decays
+// with states of 1e12: 557 us forward for 311).
+constexpr float kLift = 4294967296.f, kMaxF = 3.4028235e38f;
 struct Joint {
   float2 P, H;
 };
@@ -345,11 +346,11 @@ __device__ __forceinline__ float2 apply(const Joint& a, float2 h) {
 }
 __device__ __forceinline__ void join(Joint& a, const Span& s) {
   a.H = apply(s, a.H);
-  a.P = mul2(a.P, s.P);
+  a.P = mul2_ftz(a.P, s.P);
 }
 __device__ __forceinline__ void join(Joint& a, const Joint& s) {
   a.H = apply(s, a.H);
-  a.P = mul2(mul2(a.P, s.P), splat(1.f / kLift));
+  a.P = mul2_ftz(mul2(a.P, s.P), splat(1.f / kLift));
 }
 // The larger of m and both magnitudes; NaN if one is.
 __device__ __forceinline__ float peak(float m, float2 h) {
@@ -414,7 +415,7 @@ __device__ __forceinline__ float2 one_by_one(const GatedRec* tot, int n, uint64_
   }
   return h;
 }
-template <int NWMAX, typename Total>
+template <bool GROWS, int NWMAX, typename Total>
 __device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, int pos, uint64_t tag, float2 first,
                                               Front<NWMAX>& fr, const Total& own) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, NW = blockDim.x >> 5;
@@ -457,7 +458,9 @@ __device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, in
       float2 P, H = first;
       if (grp > 0) rec_wait(head_rec(p, item, pos), tag, P, H, p);
       float2 after = apply(a, H);
-      if (!(peak(peak(m, H), after) < kLift)) after = apply(tot, one_by_one(tots, n, tag, H));
+      m = peak(peak(m, H), after);
+      if (!(m < kLift) && !(m <= kMaxF && (!GROWS || (a.P.x > 0.f && a.P.y > 0.f))))
+        after = apply(tot, one_by_one(tots, n, tag, H));
       rec_put(p, p.pre, ((size_t)item * p.ngrp + grp) * kGatedCG + lane * 2, (size_t)p.B * p.NG * p.ngrp * kGatedCG,
               splat(0.f), after, tag);
       fr.h[lane] = H;
@@ -470,7 +473,10 @@ __device__ __forceinline__ float2 gated_front(const GatedParams& p, int item, in
     h = apply(fr.part[i][lane], h);
     m = peak(m, h);
   }
-  return m < kLift ? h : one_by_one(tots, n, tag, fr.h[lane]);
+  if (m < kLift) return h;
+  bool whole = m <= kMaxF;
+  for (int i = 0; GROWS && i * per < n; ++i) whole &= fr.part[i][lane].P.x > 0.f && fr.part[i][lane].P.y > 0.f;
+  return whole ? h : one_by_one(tots, n, tag, fr.h[lane]);
 }
 
 // The tiles of a CTA. Several tiles per sequence: by tickets, so that every
@@ -597,7 +603,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_fwd(const 
     const float2 first = a.pos == 0 ? sh.first[par][lane] : splat(0.f);
     float2 h;  // the state in front of the tile
     if (chained && p.G > 1) {
-      h = gated_front<NWMAX>(p, a.item, a.pos, tag, first, sh.front, [&] {
+      h = gated_front<GATE == kGateDecay>(p, a.item, a.pos, tag, first, sh.front, [&] {
         Span tot = sh.agg[par][0][lane];
         for (int i = 1; i < NW; ++i) {
           const Span u = sh.agg[par][i][lane];
@@ -758,7 +764,7 @@ __global__ void __launch_bounds__(32 * NWMAX, 64 / (NWMAX * 4)) gated_bwd(const 
     const float2 first = a.pos == 0 ? sh.first[par][lane] : splat(0.f);
     float2 q;  // f_{t+1} D_{t+1}, what flows back into token t
     if (chained && p.G > 1) {
-      q = gated_front<NWMAX>(p, a.item, a.pos, tag, first, sh.front, [&] {
+      q = gated_front<GATE == kGateDecay>(p, a.item, a.pos, tag, first, sh.front, [&] {
         Span tot{sh.agg[par][NW - 1][lane].P, sh.rev[par][NW - 1][lane]};
         for (int i = NW - 2; i >= 0; --i) {
           const Span u{sh.agg[par][i][lane].P, sh.rev[par][i][lane]};
